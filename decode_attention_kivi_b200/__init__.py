@@ -26,6 +26,8 @@ __all__ = [
     "kivi_decode_attention_static_scratch", "kivi_static_scratch_status",
     "kivi_bf16_workspace_bytes", "kivi_bf16_decode_attention", "kivi_bf16_status",
     "Bf16Attention", "kivi_fake_quant_keys", "kivi_prefill_attention", "kivi_causal_attention",
+    "kivi_paged_assign", "kivi_paged_append", "kivi_paged_attention", "kivi_packed_attention",
+    "kivi_attention_workspace_bytes", "kivi_attention_status", "PackedAttention", "PagedCache",
 ]
 
 GROUP_SIZE = 32
@@ -281,6 +283,245 @@ class Bf16Attention:
 
     def check_device_status(self, stream=None) -> int:
         return kivi_bf16_status(self.workspace, self.B, self.Hkv, stream)
+
+
+# ---- the paged 16-bit cache and attention over packed rows ----
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # KIVI_BF16, KIVI_FP16
+
+
+def _one_device(first: torch.Tensor, *rest) -> None:
+    """All tensors on one CUDA device, the current one (whose stream the call takes)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but cuda:{torch.cuda.current_device()} is current")
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between rows of t [rows][heads][channels]: a row is contiguous, rows may be apart
+    (a slice of a wider projection)."""
+    _, heads, dim = t.shape
+    row, head, chan = t.stride()
+    if (chan != 1 and dim > 1) or (head != dim and heads > 1):
+        raise ValueError(f"{name}: heads and channels of a row must be contiguous")
+    return heads * dim if t.shape[0] < 2 else row
+
+
+def _new_out(q: torch.Tensor, stream) -> torch.Tensor:
+    """An output of q's shape that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+
+
+def _int_array(t: torch.Tensor, shape, name: str) -> int:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _pages(k_pages, v_pages, dtype=None):
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        raise ValueError("pages: k and v [num_pages][Hkv][page_size][D]")
+    if k_pages.dtype not in _DTYPES or v_pages.dtype != k_pages.dtype \
+            or (dtype is not None and k_pages.dtype != dtype):
+        raise ValueError(f"pages must be bf16 or fp16 like the rows, got {k_pages.dtype}")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("pages must be contiguous")
+    return k_pages.shape
+
+
+def kivi_attention_workspace_bytes(num_kv_heads: int, num_q_heads: int, head_dim: int) -> int:
+    """Bytes of the (zero-filled) workspace of the packed and paged attention calls."""
+    n = ctypes.c_size_t()
+    check(lib().kivi_attention_workspace_bytes(num_kv_heads, num_q_heads, head_dim,
+                                               ctypes.byref(n)), "kivi_attention_workspace_bytes")
+    return n.value
+
+
+def kivi_attention_status(workspace: torch.Tensor, stream=None) -> int:
+    """Reads and clears the status word of an attention workspace (0: nothing reported)."""
+    code = ctypes.c_uint32()
+    rc = lib().kivi_attention_status(_ptr(workspace, name="workspace"), _stream(stream),
+                                     ctypes.byref(code))
+    if rc not in (0, 7):
+        check(rc, "kivi_attention_status")
+    return code.value
+
+
+def kivi_paged_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor,
+                      free_pages: torch.Tensor, num_free: torch.Tensor, page_size: int, *,
+                      kv_lengths: torch.Tensor, num_free_out: torch.Tensor, offsets: torch.Tensor,
+                      slots: torch.Tensor, positions: torch.Tensor, status: torch.Tensor,
+                      stream=None) -> None:
+    """Block tables, slot map and positions of a step on the device (see kivi.h): extends
+    block_table [B][W] from the stack free_pages / num_free by what new_tokens [B] need beyond
+    lengths [B], and fills kv_lengths [B], num_free_out [1], offsets [B+1], slots and positions
+    [rows].  Negative new_tokens release a request.  All int32; `status` [1] collects failures."""
+    _one_device(lengths, new_tokens, block_table, free_pages, num_free, kv_lengths, num_free_out,
+                offsets, slots, positions, status)
+    if block_table.dim() != 2 or free_pages.dim() != 1 or slots.dim() != 1:
+        raise ValueError("block_table [B][W], free_pages [num_pages], slots [rows]")
+    B, width = block_table.shape
+    pages, rows = free_pages.shape[0], slots.shape[0]
+    check(lib().kivi_paged_assign(
+        _int_array(lengths, (B,), "lengths"), _int_array(new_tokens, (B,), "new_tokens"), B,
+        _int_array(block_table, (B, width), "block_table"), width,
+        _int_array(free_pages, (pages,), "free_pages"), _int_array(num_free, (1,), "num_free"),
+        pages, page_size, _int_array(kv_lengths, (B,), "kv_lengths"),
+        _int_array(num_free_out, (1,), "num_free_out"), _int_array(offsets, (B + 1,), "offsets"),
+        _int_array(slots, (rows,), "slots"), _int_array(positions, (rows,), "positions"), rows,
+        _int_array(status, (1,), "status"), _stream(stream)), "kivi_paged_assign")
+
+
+def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
+                      k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      status: torch.Tensor | None = None, stream=None) -> None:
+    """Writes k_new, v_new [rows][Hkv][D] into the slots [rows] of one layer's pages
+    [num_pages][Hkv][page_size][D] (bf16 or fp16); rows with a negative slot are skipped."""
+    _one_device(k_new, v_new, slots, k_pages, v_pages, status)
+    pages, hkv, page, dim = _pages(k_pages, v_pages, k_new.dtype)
+    rows = k_new.shape[0]
+    if k_new.shape != (rows, hkv, dim) or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must be [rows][Hkv][D] of the pages' type")
+    check(lib().kivi_paged_append(
+        k_new.data_ptr(), _row_stride(k_new, "k_new"), v_new.data_ptr(),
+        _row_stride(v_new, "v_new"), _int_array(slots, (rows,), "slots"), rows,
+        k_pages.data_ptr(), v_pages.data_ptr(), pages, page, hkv, dim,
+        None if status is None else _int_array(status, (1,), "status"), _stream(stream)),
+        "kivi_paged_append")
+
+
+def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                          offsets: torch.Tensor, workspace: torch.Tensor,
+                          out: torch.Tensor | None = None, sm_scale: float = 0.0,
+                          stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts: q [rows][Hq][D], k and v [rows][Hkv][D] (bf16 or fp16),
+    request b in rows offsets[b] .. offsets[b+1]-1 (int32, on the device) -> out like q.  Rows
+    behind the last request are left as they were."""
+    _one_device(q, k, v, offsets, workspace, out)
+    if out is None:
+        out = _new_out(q, stream)
+    rows, hq, dim = q.shape
+    hkv = k.shape[1]
+    if k.shape != (rows, hkv, dim) or v.shape != k.shape or out.shape != q.shape:
+        raise ValueError("shapes: q and out [rows][Hq][D], k and v [rows][Hkv][D]")
+    if q.dtype not in _DTYPES or not (q.dtype == k.dtype == v.dtype == out.dtype):
+        raise ValueError(f"q, k, v and out must all be bf16 or all fp16, got {q.dtype}")
+    B = offsets.numel() - 1
+    check(lib().kivi_packed_attention(
+        q.data_ptr(), _row_stride(q, "q"), k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
+        _row_stride(v, "v"), out.data_ptr(), _row_stride(out, "out"), _DTYPES[q.dtype],
+        _int_array(offsets, (B + 1,), "offsets"), B, rows, hkv, hq, dim, float(sm_scale),
+        _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "kivi_packed_attention")
+    return out
+
+
+def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         block_table: torch.Tensor, kv_lengths: torch.Tensor,
+                         offsets: torch.Tensor, workspace: torch.Tensor,
+                         max_new: int | None = None, out: torch.Tensor | None = None,
+                         sm_scale: float = 0.0, stream=None) -> torch.Tensor:
+    """Attention of each request's new rows (q [rows][Hq][D], request b in rows offsets[b] ..
+    offsets[b+1]-1) over its kv_lengths[b] keys in the pages of block_table[b], causal, the new
+    tokens being the last keys -> out like q.  max_new: no request has more new rows (1 in a
+    decode step; by default the number of rows)."""
+    _one_device(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, out)
+    if out is None:
+        out = _new_out(q, stream)
+    rows, hq, dim = q.shape
+    pages, hkv, page, pdim = _pages(k_pages, v_pages, q.dtype)
+    if pdim != dim or out.shape != q.shape or out.dtype != q.dtype or block_table.dim() != 2:
+        raise ValueError("shapes: q and out [rows][Hq][D], pages [num_pages][Hkv][page_size][D]")
+    B, width = block_table.shape
+    check(lib().kivi_paged_attention(
+        q.data_ptr(), _row_stride(q, "q"), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+        _row_stride(out, "out"), _DTYPES[q.dtype],
+        _int_array(block_table, (B, width), "block_table"), width,
+        _int_array(kv_lengths, (B,), "kv_lengths"), _int_array(offsets, (B + 1,), "offsets"), B,
+        rows, max(rows, 1) if max_new is None else int(max_new), pages, page, hkv, hq, dim,
+        float(sm_scale), _ptr(workspace, name="workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "kivi_paged_attention")
+    return out
+
+
+class PackedAttention:
+    """Owns the workspace of kivi_packed_attention for one head layout."""
+
+    def __init__(self, *, num_kv_heads, num_q_heads, head_dim, device="cuda"):
+        n = kivi_attention_workspace_bytes(num_kv_heads, num_q_heads, head_dim)
+        self.workspace = torch.zeros(n, dtype=torch.uint8, device=device)
+
+    def attend(self, q, k, v, offsets, out=None, sm_scale=0.0, stream=None):
+        return kivi_packed_attention(q, k, v, offsets, self.workspace, out, sm_scale, stream)
+
+    def check_device_status(self, stream=None) -> int:
+        return kivi_attention_status(self.workspace, stream)
+
+
+class PagedCache:
+    """A paged bf16 or fp16 KV cache of up to max_requests requests: the page pool of every layer,
+    the requests' block table, lengths and free pages, and the workspace, all on the device.
+
+    A step: ``assign(new_tokens, rows)`` once, then per layer ``append(layer, k, v)`` and
+    ``attend(layer, q)``; ``offsets``, ``slots`` and ``positions`` describe the step's packed rows.
+    """
+
+    def __init__(self, *, num_pages, page_size, num_layers, num_kv_heads, num_q_heads, head_dim,
+                 max_requests, max_tokens, dtype=torch.bfloat16, device="cuda"):
+        self.page_size = page_size
+        dev = torch.device(device)
+        shape = (num_layers, num_pages, num_kv_heads, page_size, head_dim)
+        n = kivi_attention_workspace_bytes(num_kv_heads, num_q_heads, head_dim)
+        self.k_pages = torch.empty(shape, dtype=dtype, device=dev)
+        self.v_pages = torch.empty(shape, dtype=dtype, device=dev)
+        self.block_table = torch.zeros(max_requests, -(-max_tokens // page_size),
+                                       dtype=torch.int32, device=dev)
+        self.lengths = torch.zeros(max_requests, dtype=torch.int32, device=dev)
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=dev)
+        self.num_free = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
+        self.offsets = torch.zeros(max_requests + 1, dtype=torch.int32, device=dev)
+        self.slots = self.positions = torch.zeros(0, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.workspace = torch.zeros(n, dtype=torch.uint8, device=dev)
+        self.max_new = 1
+
+    def assign(self, new_tokens: torch.Tensor, rows: int, max_new: int | None = None,
+               stream=None) -> None:
+        """Starts a step: new_tokens [max_requests] (int32, device; negative releases), `rows`
+        packed rows in the step's buffers, of which no request has more than max_new."""
+        if rows != self.slots.numel():  # kept from step to step while the size stays
+            self.slots = torch.empty(rows, dtype=torch.int32, device=self.lengths.device)
+            self.positions = torch.empty_like(self.slots)
+        self.max_new = rows if max_new is None else max_new
+        kivi_paged_assign(self.lengths, new_tokens, self.block_table, self.free_pages,
+                          self.num_free, self.page_size, kv_lengths=self.lengths,
+                          num_free_out=self.num_free, offsets=self.offsets, slots=self.slots,
+                          positions=self.positions, status=self.status, stream=stream)
+
+    def append(self, layer, k_new, v_new, stream=None):
+        kivi_paged_append(k_new, v_new, self.slots, self.k_pages[layer], self.v_pages[layer],
+                          self.status, stream)
+
+    def attend(self, layer, q, out=None, sm_scale=0.0, stream=None):
+        return kivi_paged_attention(q, self.k_pages[layer], self.v_pages[layer], self.block_table,
+                                    self.lengths, self.offsets, self.workspace, self.max_new, out,
+                                    sm_scale, stream)
+
+    def check_device_status(self, stream=None) -> int:
+        """The step's failures (bits of kivi.h) since the last query; clears them."""
+        code = kivi_attention_status(self.workspace, stream) | int(self.status.item())
+        self.status.zero_()
+        return code
 
 
 def kivi_status_string(code: int) -> str:

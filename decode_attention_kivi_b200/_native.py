@@ -45,7 +45,7 @@ def lib() -> ctypes.CDLL:
             f"{_LIB_PATH} is missing: build it with `python -m decode_attention_kivi_b200.build` "
             "(there is no CPU fallback)")
     L = ctypes.CDLL(_LIB_PATH)
-    P, I32, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+    P, I32, I64, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     st = ctypes.c_int
     sig = {
         "kivi_required_bytes": (st, [ctypes.POINTER(KiviConfig), ctypes.POINTER(KiviSizes)]),
@@ -77,6 +77,14 @@ def lib() -> ctypes.CDLL:
         "kivi_fake_quant_keys": (st, [P, ctypes.c_int64, I32, I32, I32, P, P]),
         "kivi_prefill_attention": (st, [P, I32, P, P, P, I32, P, F32, P]),
         "kivi_causal_attention": (st, [P, P, P, I32, I32, I32, I32, I32, P, F32, P, P]),
+        "kivi_paged_assign": (st, [P, P, I32, P, I32, P, P, I32, I32, P, P, P, P, P, I32, P, P]),
+        "kivi_paged_append": (st, [P, I64, P, I64, P, I32, P, P, I32, I32, I32, I32, P, P]),
+        "kivi_attention_workspace_bytes": (st, [I32, I32, I32, ctypes.POINTER(ctypes.c_size_t)]),
+        "kivi_packed_attention": (st, [P, I64, P, I64, P, I64, P, I64, I32, P, I32, I32, I32, I32,
+                                       I32, F32, P, ctypes.c_size_t, P]),
+        "kivi_paged_attention": (st, [P, I64, P, P, P, I64, I32, P, I32, P, P, I32, I32, I32, I32,
+                                      I32, I32, I32, I32, F32, P, ctypes.c_size_t, P]),
+        "kivi_attention_status": (st, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
     }
     if hasattr(L, "kivi_debug_overstate_copies"):  # debug build only
         sig["kivi_debug_overstate_copies"] = (st, [ctypes.c_uint32])

@@ -370,6 +370,130 @@ kivi_status kivi_bf16_status(void* workspace, int32_t batch, int32_t num_kv_head
 kivi_status kivi_fake_quant_keys(const void* k, int64_t rows, int32_t head_dim, int32_t bits,
                                  int32_t per_token, float* k_hat, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The paged 16-bit cache and attention over packed rows                     */
+/* ------------------------------------------------------------------------ */
+
+/* A step of a server: B requests, each with some new tokens (a prompt, a chunk
+ * of one, or the one token it decodes).  The step's rows are packed without
+ * padding, request b in rows offsets[b] .. offsets[b+1]-1; a buffer may hold
+ * more rows than offsets[B], which no call reads or writes.  Keys and values lie
+ * in pages of page_size tokens from one pool per layer,
+ *   k_pages, v_pages: [num_pages][num_kv_heads][page_size][head_dim],
+ * token j of request b in page block_table[b][j / page_size]; a slot is
+ * page * page_size + token within the page.  In call order: kivi_paged_assign
+ * once per step, then for each layer kivi_paged_append and
+ * kivi_paged_attention; or kivi_packed_attention for whole prompts, which needs
+ * no pages.  The length arrays are on the device and no call waits for them, so
+ * a step can be captured into a CUDA graph and replayed.
+ *
+ * Elements are bf16 or fp16 (KIVI_BF16, KIVI_FP16), the same for all operands of
+ * a call and for its output.  page_size: 16, 32, 64, 128 or 256.  head_dim: 64
+ * or 128.  num_q_heads / num_kv_heads: any whole number up to 128.  At most 4096
+ * requests.  Row strides are in elements, multiples of 8 and at least heads *
+ * head_dim; heads and channels of a row are contiguous.
+ *
+ * What the device arrays hold cannot be refused by a call; a value outside its
+ * buffer is clamped, touches no memory outside, and sets a bit of the call's
+ * status word (bits stay set until the caller clears the word):
+ *   1  a bounded wait ran out (results invalid)
+ *   2  a page id or slot outside the pool (its keys and values read as zeros; the
+ *      slot is not written)
+ *   4  offsets or lengths outside their buffers or decreasing, a request with
+ *      more new tokens than keys or than max_new
+ *   8  not enough free pages */
+#define KIVI_BF16 0
+#define KIVI_FP16 1
+#define KIVI_PAGED_TIMEOUT 1u
+#define KIVI_PAGED_BAD_PAGE 2u
+#define KIVI_PAGED_BAD_LENGTH 4u
+#define KIVI_PAGED_NO_PAGES 8u
+
+/* Block tables, slot map and positions of a step, all on the device (int32).
+ *   lengths[batch]: tokens each request holds; new_tokens[batch]: tokens it adds
+ *     in this step, 0 for none, negative to release it (its pages go back).
+ *   block_table[batch][table_width]: a request's first ceil(length / page_size)
+ *     entries are its pages; the new ones are written behind them.
+ *   free_pages[num_pages], num_free[1]: the free pages, a stack.  Released pages
+ *     are pushed in request order, then the step's new pages are popped one by
+ *     one in request order.
+ *   kv_lengths[batch]: the lengths after the step (0 for a released request); may
+ *     be `lengths`.  num_free_out[1] may be `num_free`.
+ *   offsets[batch + 1]: prefix sums of the new tokens.
+ *   slots[rows], positions[rows]: of each packed row; -1 and 0 for the rows behind
+ *     the last request's.
+ *   status: a word as above.  If the pages do not suffice (8), or a length, the
+ *     new rows (more than `rows`) or the free count do not fit (4), nothing
+ *     changes: kv_lengths and num_free_out repeat the old values, offsets are 0
+ *     and slots -1, so the step's other calls do nothing.
+ * Apart from the two pairs named the arrays must not overlap.
+ * Errors: INVALID_ARG (NULL or unaligned pointers, counts, table_width * page_size
+ * or num_pages * page_size >= 2^31 - 256), UNSUPPORTED (page_size, batch), CUDA. */
+kivi_status kivi_paged_assign(const int32_t* lengths, const int32_t* new_tokens, int32_t batch,
+                              int32_t* block_table, int32_t table_width, int32_t* free_pages,
+                              const int32_t* num_free, int32_t num_pages, int32_t page_size,
+                              int32_t* kv_lengths, int32_t* num_free_out, int32_t* offsets,
+                              int32_t* slots, int32_t* positions, int32_t rows, uint32_t* status,
+                              void* stream);
+
+/* Writes the keys and values of `rows` packed rows into their slots of one
+ * layer's pages: k_new, v_new [rows][num_kv_heads][head_dim] of any 16-bit type.
+ * A slot of -1 (any negative) is skipped, one outside the pool is skipped and
+ * sets bit 2 of `status` (NULL: not reported).  No two rows may have the same
+ * slot.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+kivi_status kivi_paged_append(const void* k_new, int64_t k_stride, const void* v_new,
+                              int64_t v_stride, const int32_t* slots, int32_t rows, void* k_pages,
+                              void* v_pages, int32_t num_pages, int32_t page_size,
+                              int32_t num_kv_heads, int32_t head_dim, uint32_t* status,
+                              void* stream);
+
+/* Workspace bytes of the two attention calls below: a status header (256 B, the
+ * word first) and the partial results of rows whose keys are split.  Host only.
+ * The header must be zero-filled before first use; calls that share a workspace
+ * must not overlap on the GPU (two captured graphs that may run side by side need
+ * one each).  Errors: INVALID_ARG, UNSUPPORTED (head_dim, head ratio). */
+kivi_status kivi_attention_workspace_bytes(int32_t num_kv_heads, int32_t num_q_heads,
+                                           int32_t head_dim, size_t* bytes);
+
+/* Causal attention of packed prompts: for row t of request b and query head h,
+ *   out[t][h] = sum_j softmax_j(sm_scale * <q[t][h], k[j][kvh]>) v[j][kvh]
+ * over the rows j of the same request up to t, kvh = h / (num_q_heads /
+ * num_kv_heads).  fp32 scores, statistics and accumulation; the softmax weights
+ * are rounded to the element type for the second product, the result once.
+ *   q, out: [rows][num_q_heads][head_dim]; k, v: [rows][num_kv_heads][head_dim].
+ *   sm_scale <= 0 means 1/sqrt(head_dim).
+ * Inputs of a request must be finite; rows of no request may hold anything.
+ * Errors: INVALID_ARG, UNSUPPORTED, BUFFER_TOO_SMALL (workspace), CUDA. */
+kivi_status kivi_packed_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, void* out, int64_t out_stride,
+                                  int32_t dtype, const int32_t* offsets, int32_t batch,
+                                  int32_t rows, int32_t num_kv_heads, int32_t num_q_heads,
+                                  int32_t head_dim, float sm_scale, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Attention of each request's new tokens over its pages.  Request b holds
+ * kv_lengths[b] keys, the step's among them (appended before this call); its
+ * row i of n sees keys 0 .. kv_lengths[b] - n + i.  A row without keys is 0.
+ * max_new: no request of the step has more new rows (1 for a decode step); a
+ * request that has more is not computed and sets bit 4.  What the pages hold
+ * behind a request's last key may be anything.  Otherwise as
+ * kivi_packed_attention.
+ * Errors: INVALID_ARG (also num_pages * page_size * num_kv_heads >= 2^31),
+ * UNSUPPORTED, BUFFER_TOO_SMALL (workspace), CUDA. */
+kivi_status kivi_paged_attention(const void* q, int64_t q_stride, const void* k_pages,
+                                 const void* v_pages, void* out, int64_t out_stride, int32_t dtype,
+                                 const int32_t* block_table, int32_t table_width,
+                                 const int32_t* kv_lengths, const int32_t* offsets, int32_t batch,
+                                 int32_t rows, int32_t max_new, int32_t num_pages,
+                                 int32_t page_size, int32_t num_kv_heads, int32_t num_q_heads,
+                                 int32_t head_dim, float sm_scale, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Synchronises `stream`, reads the status word of an attention workspace and
+ * clears it if it is not zero.  KIVI_ERR_DEVICE if it was set, KIVI_ERR_CUDA if a
+ * CUDA call failed, else KIVI_OK; `code_out` may be NULL. */
+kivi_status kivi_attention_status(void* workspace, void* stream, uint32_t* code_out);
+
 /* Static text for a status code; never NULL. */
 const char* kivi_status_string(kivi_status status);
 
