@@ -11,6 +11,12 @@ namespace kivi {
 constexpr int kMaxRequests = 4096;   // requests of one call (their prefix sums sit in shared memory)
 constexpr int kMinPage = 16, kMaxPage = 256;
 
+// Workspace of the attention calls: the status word, tickets from byte 64 on, and from
+// kPagedHeader on the partials of at most kMaxGrid CTAs.
+constexpr int kMaxGrid = 160;
+constexpr int kPagedHeader = 1024;
+static_assert(64 + 4 * kMaxGrid <= kPagedHeader, "tickets");
+
 // Bits of a status word (a call ORs them in; KIVI_PAGED_* in kivi.h).
 constexpr uint32_t kPagedTimeout = 1u;     // a bounded wait ran out
 constexpr uint32_t kPagedBadPage = 2u;     // a page id or slot outside the pool
@@ -58,7 +64,8 @@ struct VarlenAttnArgs {
   const int* offsets;  // [B + 1]
   const int* kv_lengths;  // [B], paged only
   const int* table;       // [B][width], paged only
-  uint32_t* status;       // workspace header
+  uint32_t* status;       // workspace header: the status word,
+  int* tickets;           // then one ticket per CTA, zero between calls
   uint8_t* partials;      // the rest of the workspace
   long q_stride, k_stride, v_stride, out_stride;  // elements between rows (k, v: packed only)
   int dtype;              // 0 bf16, 1 fp16
@@ -69,5 +76,10 @@ struct VarlenAttnArgs {
   int num_sms, device;
 };
 cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream);
+long varlen_partial_bytes(int D);
+
+// The requests of few rows (paged form only); scale_log2 = scale * log2 e.
+cudaError_t launch_paged_decode(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream);
+long paged_decode_partial_bytes(int D);
 
 }  // namespace kivi

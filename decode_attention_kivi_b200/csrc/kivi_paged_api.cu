@@ -5,7 +5,6 @@
 #include <cmath>
 
 #include "../../include/kivi.h"
-#include "kivi_layout.cuh"
 #include "kivi_paged.h"
 
 namespace {
@@ -75,7 +74,8 @@ kivi_status attention_args(kivi::VarlenAttnArgs& a, int32_t dtype, const void* q
   a.out_stride = out_stride;
   a.offsets = offsets;
   a.status = static_cast<uint32_t*>(workspace);
-  a.partials = static_cast<uint8_t*>(workspace) + kivi::kWsHeader;
+  a.tickets = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + 64);
+  a.partials = static_cast<uint8_t*>(workspace) + kivi::kPagedHeader;
   a.dtype = dtype;
   a.B = batch;
   a.T = rows;
@@ -163,7 +163,7 @@ kivi_status kivi_attention_workspace_bytes(int32_t num_kv_heads, int32_t num_q_h
   if (!bytes) return KIVI_ERR_INVALID_ARG;
   const kivi_status st = heads_of(num_kv_heads, num_q_heads, head_dim);
   if (st != KIVI_OK) return st;
-  *bytes = kivi::kWsHeader;
+  *bytes = kivi::kPagedHeader + (size_t)kivi::varlen_partial_bytes(head_dim);
   return KIVI_OK;
 }
 
@@ -228,7 +228,8 @@ kivi_status kivi_attention_status(void* workspace, void* stream, uint32_t* code_
   uint32_t code = 0;
   if (cudaMemcpy(&code, workspace, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess)
     return KIVI_ERR_CUDA;
-  if (code != 0 && cudaMemset(workspace, 0, kivi::kWsHeader) != cudaSuccess) return KIVI_ERR_CUDA;
+  if (code != 0 && cudaMemset(workspace, 0, kivi::kPagedHeader) != cudaSuccess)
+    return KIVI_ERR_CUDA;
   if (code_out) *code_out = code;
   return code ? KIVI_ERR_DEVICE : KIVI_OK;
 }

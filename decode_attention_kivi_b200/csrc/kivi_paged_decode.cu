@@ -1,0 +1,504 @@
+// kivi_paged_decode.cu - attention of single tokens (and of a few at once) over
+// a paged 16-bit cache.
+//
+// A request with n new rows and g query heads per kv head, n * g <= 16, gives
+// one tensor tile of 16 rows (token i, head h at row i * g + h) per kv head that
+// reads the request's keys once: 4 D bytes per key against 4 D g n FLOPs, so the
+// bound is HBM.  The tiles of 64 keys of all (request, kv head) items, in order,
+// are cut into one contiguous range per CTA, equal to within a tile whatever the
+// lengths are; the prefix sums over the requests that this needs are formed by
+// every CTA from the device arrays.
+//
+// Each CTA (one per SM) has a producer warp that streams K and V through a ring
+// of stages with 2D tensor copies, one box of min(page, 64) rows x 64 channels
+// per lane, the page ids read by the lane that needs them.  Four consumer warps
+// take 16 keys of every tile each, on the tensor cores (mma.sync m16n8k16, fp32
+// accumulation): S[row][key] = Q K^T with Q in registers, an online softmax in
+// base 2 whose weights stay in registers as the operand of O[row][chan] += P V.
+// The four states are merged when the item ends.  An item that lies in several
+// CTAs leaves a partial (m, l, O in fp32) per CTA; the last CTA to arrive (a
+// ticket per CTA that begins such an item) joins them in CTA order, so results
+// do not depend on the order of arrival.
+// Every wait is bounded; a wait that runs out sets the status word.
+#include "kivi_launch.cuh"
+#include "kivi_varlen.cuh"
+
+namespace kivi {
+namespace {
+
+constexpr float kLog2eD = 1.4426950408889634f;
+constexpr int kTileD = 64;          // keys per tile
+constexpr int kWarpsD = 4;          // consumer warps, 16 keys of each tile
+constexpr int kThreadsD = (kWarpsD + 1) * 32;
+constexpr int kBoxD = kTileD * 128; // 64 rows of 64 channels, the swizzle span
+constexpr int kMinTilesD = 2;       // tiles per CTA at least
+
+template <int D>
+struct DCfg {
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kTileBytes = kSlabs * kBoxD;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = (160 * 1024) / kStageBytes;
+  static constexpr int kState = kDecodeRows * (D + 2);  // O[16][D], m[16], l[16]
+  static constexpr int kOffMerge = kStages * kStageBytes;
+  static constexpr int kOffBars = kOffMerge + kWarpsD * kState * 4;
+  static constexpr int kOffPrefix = kOffBars + 2 * kStages * 8 + 64;
+  static constexpr int bytes(int B) { return kOffPrefix + 4 * (B + 1) + 1024; }
+  static_assert(bytes(kMaxRequests) <= 227 * 1024, "shared-memory plan");
+};
+
+// Tiles of one (request, kv head); a request without keys has one, for its zeros.
+__device__ __forceinline__ int tiles_of(const Request& r) {
+  return r.L > 0 ? (r.L + kTileD - 1) / kTileD : 1;
+}
+
+struct Split {
+  int n, q, rem;  // CTAs with work; total = n * q + rem
+  __device__ __forceinline__ int lo(int c) const { return c * q + min(c, rem); }
+  __device__ __forceinline__ int cta_of(int t) const {
+    const int big = rem * (q + 1);
+    return t < big ? t / (q + 1) : rem + (t - big) / q;
+  }
+};
+
+// The position of a CTA in its range: request b, kv head, tile j of nt.
+struct Cursor {
+  int b, kvh, j, nt;
+  Request r;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsD, 1)
+paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    VarlenAttnArgs a, float scale_log2) {
+  using C = DCfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+  uint64_t* empty = full + C::kStages;
+  int* s_flag = reinterpret_cast<int*>(empty + C::kStages);  // the ticket's verdict
+  volatile int* s_abort = s_flag + 1;
+  volatile int* s_issued = s_flag + 2;
+  int* s_sum = s_flag + 4;  // [kWarpsD + 1] sums of the scan
+  int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hpk = a.Hq / a.Hkv;
+
+  if (threadIdx.x == 0) {
+    *s_abort = 0;
+    *s_issued = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarpsD);
+    }
+    fence_mbar_init();
+  }
+  wait_for_predecessor();
+
+  // ---- prefix sums of the requests' tiles ----
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreadsD) {
+    const int b = b0 + threadIdx.x;
+    int v = 0;
+    if (b < a.B) {
+      bool bad = false;
+      const Request r = load_request(a, b, &bad);
+      if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
+      if (r.n > 0 && is_short(r.n, hpk)) v = a.Hkv * tiles_of(r);
+    }
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w <= kWarpsD; ++w) {
+      if (w < warp) before += s_sum[w];
+      all += s_sum[w];
+    }
+    if (b < a.B) prefix[b] = base + before + inc - v;
+    base += all;
+  }
+  if (threadIdx.x == 0) prefix[a.B] = base;
+  __syncthreads();
+  Split sp;
+  sp.n = min((int)gridDim.x, (base + kMinTilesD - 1) / kMinTilesD);
+  if ((int)blockIdx.x >= sp.n) return;
+  sp.q = base / sp.n;
+  sp.rem = base - sp.n * sp.q;
+  const int cta = blockIdx.x, t_begin = sp.lo(cta), n_tiles = sp.lo(cta + 1) - t_begin;
+
+  auto enter = [&](Cursor& c, int b) {
+    bool bad;
+    c.b = b;
+    c.r = load_request(a, b, &bad);
+    c.nt = tiles_of(c.r);
+  };
+  auto start = [&]() {
+    int lo = 0, hi = a.B;  // largest b with prefix[b] <= t_begin
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= t_begin) lo = mid;
+      else hi = mid;
+    }
+    Cursor c;
+    enter(c, lo);
+    const int t = t_begin - prefix[lo];
+    c.kvh = t / c.nt;
+    c.j = t - c.kvh * c.nt;
+    return c;
+  };
+  // moves on by a tile; true when that begins another item
+  auto next = [&](Cursor& c) {
+    if (++c.j < c.nt) return false;
+    c.j = 0;
+    if (++c.kvh == a.Hkv) {
+      int b = c.b + 1;
+      while (prefix[b + 1] == prefix[b]) ++b;  // the caller has tiles left
+      enter(c, b);
+      c.kvh = 0;
+    }
+    return true;
+  };
+
+  if (warp == kWarpsD) {
+    // ---- producer ----
+    const int page = 1 << a.page_shift, rows = page < kTileD ? page : kTileD;
+    const int per_tile = kTileD / rows;           // boxes of a slab
+    const int boxes = per_tile * C::kSlabs * 2;   // of a stage, one per lane (at most 16)
+    const int is_v = lane & 1, slab = (lane >> 1) % C::kSlabs, part = (lane >> 1) / C::kSlabs;
+    const int outside = (a.num_pages * a.Hkv) << a.page_shift;  // a row that reads as zero
+    const CUtensorMap* map = is_v ? &tv : &tk;
+    Cursor c = start();
+    int issued = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int s = i % C::kStages;
+      if (i > 0) next(c);
+      const int key = c.j * kTileD + part * rows;  // this lane's first key
+      const bool mine = lane < boxes && key < c.r.L;
+      int y = outside;
+      if (mine) {
+        const int id = a.table[(long)c.b * a.width + (key >> a.page_shift)];
+        if (id >= 0 && id < a.num_pages)
+          y = ((id * a.Hkv + c.kvh) << a.page_shift) + (key & (page - 1));
+        else
+          atomicOr(a.status, kPagedBadPage);
+      }
+      bool ok = *s_abort == 0;
+      if (ok && i >= C::kStages) ok = mbar_wait_bounded(&empty[s], (uint32_t)((i / C::kStages) - 1) & 1u);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) {
+          atomicOr(a.status, kPagedTimeout);
+          *s_abort = 1;
+        }
+        break;
+      }
+      const int n = __popc(__ballot_sync(0xffffffffu, mine));
+      unsigned char* st = smem + s * C::kStageBytes;
+      if (lane == 0) mbar_expect_tx(&full[s], n * rows * 128);
+      __syncwarp();
+      if (mine)
+        tma_load_2d(st + is_v * C::kTileBytes + slab * kBoxD + part * rows * 128, map, 64 * slab, y,
+                    &full[s]);
+      issued = i + 1;
+    }
+    if (lane == 0) *s_issued = issued;
+    __syncwarp();
+    named_sync(2, kThreadsD);
+    return;
+  }
+
+  // ---- consumers ----
+  const int g = lane >> 2, tig = lane & 3, r0 = 16 * warp;
+  constexpr int kKS = D / 16, kNT = D / 8;
+  float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+  uint32_t qf[kKS][4];
+  float o[kNT][4];
+  float m[2], l[2];  // rows g and g + 8: running maximum (log2 units), sum over this lane's keys
+  int last[2];       // the last key each row sees
+  bool dead = false;
+  int i_dead = n_tiles;
+
+  auto begin_item = [&](const Cursor& c) {
+    const int rows = c.r.n * hpk;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+      const int row = g + 8 * e, i = row / hpk;
+      const bool real = row < rows;
+      last[e] = real ? min(last_key(c.r, i), c.r.L - 1) : -1;
+      const T* qr = static_cast<const T*>(a.q) + (c.r.q0 + (real ? i : 0)) * a.q_stride +
+                    (long)(c.kvh * hpk + (real ? row - i * hpk : 0)) * D;
+#pragma unroll
+      for (int s = 0; s < kKS; ++s) {
+        const uint32_t x0 = *reinterpret_cast<const uint32_t*>(qr + 16 * s + 2 * tig);
+        const uint32_t x1 = *reinterpret_cast<const uint32_t*>(qr + 16 * s + 8 + 2 * tig);
+        qf[s][e] = real ? x0 : 0u;
+        qf[s][2 + e] = real ? x1 : 0u;
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
+  };
+
+  // O / l of the item's rows from `count` states at src(x), in order; ld reads a float or float4
+  // (other CTAs' states are read past L1).
+  auto join = [&](const Cursor& c, int count, auto src, auto ld) {
+    const int rows = c.r.n * hpk;
+    for (int x = threadIdx.x; x < rows * (D / 4); x += kWarpsD * 32) {
+      const int row = x / (D / 4), ch = x % (D / 4);
+      float M = -INFINITY;
+      for (int w = 0; w < count; ++w) M = fmaxf(M, ld(src(w) + kDecodeRows * D + row));
+      float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < count; ++w) {
+        const float* s = src(w);
+        const float mw = ld(s + kDecodeRows * D + row);
+        const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+        L += f * ld(s + kDecodeRows * (D + 1) + row);
+        const float4 q = ld(reinterpret_cast<const float4*>(s + row * D) + ch);
+        v[0] += f * q.x;
+        v[1] += f * q.y;
+        v[2] += f * q.z;
+        v[3] += f * q.w;
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;  // a row without keys is 0
+      const int i = row / hpk;
+      T* dst = static_cast<T*>(a.out) + (c.r.q0 + i) * a.out_stride +
+               (long)(c.kvh * hpk + row - i * hpk) * D + 4 * ch;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(Elem<T>::pack(v[0] * inv, v[1] * inv), Elem<T>::pack(v[2] * inv, v[3] * inv));
+    }
+  };
+  float* partials = reinterpret_cast<float*>(a.partials);
+  int* tickets = a.tickets;
+  // slot 0: the item a CTA begins in the middle of; slot 1: the one it leaves unfinished
+  auto slot = [&](int c, int which) { return partials + ((long)c * 2 + which) * C::kState; };
+
+  auto end_item = [&](const Cursor& c) {
+    float* mine = merge + warp * C::kState;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      const int row = g + 8 * e;
+      if (tig == 0) {
+        mine[kDecodeRows * D + row] = m[e];
+        mine[kDecodeRows * (D + 1) + row] = l[e];
+      }
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        *reinterpret_cast<float2*>(mine + row * D + 8 * nt + 2 * tig) =
+            make_float2(o[nt][2 * e], o[nt][2 * e + 1]);
+    }
+    named_sync(1, kWarpsD * 32);
+    const int first = prefix[c.b] + c.kvh * c.nt, final = first + c.nt - 1;
+    const bool head = first < t_begin, tail = final >= t_begin + n_tiles;
+    const int rows = c.r.n * hpk;
+    if (!head && !tail) {
+      join(c, kWarpsD, [&](int w) { return merge + w * C::kState; }, [](auto* x) { return *x; });
+      named_sync(1, kWarpsD * 32);  // the merge area is free again
+      return;
+    }
+    // one state out of the four, for the other CTAs of the item
+    float* part = slot(cta, head ? 0 : 1);
+    for (int x = threadIdx.x; x < rows * (D / 4 + 1); x += kWarpsD * 32) {
+      const int row = x / (D / 4 + 1), ch = x % (D / 4 + 1);
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarpsD; ++w) M = fmaxf(M, merge[w * C::kState + kDecodeRows * D + row]);
+      float L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarpsD; ++w) {
+        const float* s = merge + w * C::kState;
+        const float mw = s[kDecodeRows * D + row];
+        const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+        if (ch == D / 4) {
+          L += f * s[kDecodeRows * (D + 1) + row];
+        } else {
+          const float4 q = *reinterpret_cast<const float4*>(s + row * D + 4 * ch);
+          v.x += f * q.x;
+          v.y += f * q.y;
+          v.z += f * q.z;
+          v.w += f * q.w;
+        }
+      }
+      if (ch == D / 4) {
+        part[kDecodeRows * D + row] = M;
+        part[kDecodeRows * (D + 1) + row] = L;
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + 4 * ch) = v;
+      }
+    }
+    __threadfence();
+    named_sync(1, kWarpsD * 32);
+    const int c0 = sp.cta_of(first), c1 = sp.cta_of(final);
+    if (threadIdx.x == 0) *s_flag = atomicAdd(&tickets[c0], 1) == c1 - c0;
+    named_sync(1, kWarpsD * 32);
+    if (*s_flag) {
+      __threadfence();
+      // c0 leaves the item unfinished (slot 1), the others begin in its middle (slot 0)
+      join(c, c1 - c0 + 1, [&](int w) { return slot(c0 + w, w == 0 ? 1 : 0); },
+           [](auto* x) { return __ldcg(x); });
+      if (threadIdx.x == 0) tickets[c0] = 0;  // ready for the next call
+    }
+    named_sync(1, kWarpsD * 32);
+  };
+
+  Cursor c = start();
+  begin_item(c);
+  for (int i = 0; i < n_tiles; ++i) {
+    if (i > 0) {
+      const Cursor before = c;
+      if (next(c)) {
+        end_item(before);
+        begin_item(c);
+      }
+    }
+    const int s = i % C::kStages;
+    // after a wait ran out the warps keep to the same items (their merges meet on a named
+    // barrier) but consume nothing more
+    if (!dead && __any_sync(0xffffffffu, *s_abort != 0)) {
+      dead = true;
+      i_dead = i;
+    }
+    if (!dead && !__all_sync(0xffffffffu,
+                             mbar_wait_bounded(&full[s], (uint32_t)(i / C::kStages) & 1u))) {
+      dead = true;
+      i_dead = i;
+      if (lane == 0) {
+        atomicOr(a.status, kPagedTimeout);
+        *s_abort = 1;
+      }
+    }
+    if (dead) continue;
+    const int key0 = c.j * kTileD + r0;  // this warp's first key
+    const int nv = min(16, c.r.L - key0);
+    unsigned char* st = smem + s * C::kStageBytes;
+    if (nv > 0) {
+      const uint32_t kb = smem_addr(st), vb = smem_addr(st + C::kTileBytes);
+      if (nv < 16) {  // keys behind the last: their V rows must be 0 (a weight of 0 times NaN)
+        for (int x = lane; x < (16 - nv) * C::kSlabs * 8; x += 32) {
+          const int row = r0 + nv + x / (C::kSlabs * 8), rest = x % (C::kSlabs * 8);
+          *reinterpret_cast<uint4*>(st + C::kTileBytes + (rest / 8) * kBoxD + row * 128 +
+                                    16 * (rest % 8)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();  // the stage's next tensor copy comes after these writes
+        __syncwarp();
+      }
+      // ---- scores ----
+      float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int krow = r0 + (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        const int ch = 16 * ks + 8 * ((lane >> 3) & 1);
+        uint32_t kf[4];
+        ldsm_x4(kf, kb + (ch / 64) * kBoxD + krow * 128 + ((((ch % 64) >> 3) ^ (krow & 7)) << 4));
+        Elem<T>::mma(sa[0], qf[ks], kf[0], kf[1]);
+        Elem<T>::mma(sa[1], qf[ks], kf[2], kf[3]);
+      }
+      // ---- online softmax: rows g, g + 8; keys key0 + 8 nt + 2 tig + x ----
+      uint32_t p[4];
+      float al[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int key = key0 + 8 * (y >> 1) + 2 * tig + (y & 1);
+          x[y] = key <= last[e] ? sa[y >> 1][2 * e + (y & 1)] * scale_log2 : -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[e], mx), mu = mn == -INFINITY ? 0.f : mn;
+        al[e] = fast_exp2(m[e] - mu);
+        m[e] = mn;
+        float w[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) w[y] = fast_exp2(x[y] - mu);
+        l[e] = l[e] * al[e] + ((w[0] + w[1]) + (w[2] + w[3]));
+        p[e] = Elem<T>::pack(w[0], w[1]);
+        p[2 + e] = Elem<T>::pack(w[2], w[3]);
+      }
+      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          o[nt][0] *= al[0];
+          o[nt][1] *= al[0];
+          o[nt][2] *= al[1];
+          o[nt][3] *= al[1];
+        }
+      }
+      // ---- P V ----
+      const int vrow = r0 + (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+      for (int n2 = 0; n2 < kNT / 2; ++n2) {
+        const int ch = 16 * n2 + 8 * (lane >> 4);
+        uint32_t vf[4];
+        ldsm_x4_trans(vf,
+                      vb + (ch / 64) * kBoxD + vrow * 128 + ((((ch % 64) >> 3) ^ (vrow & 7)) << 4));
+        Elem<T>::mma(o[2 * n2], p, vf[0], vf[1]);
+        Elem<T>::mma(o[2 * n2 + 1], p, vf[2], vf[3]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      fence_proxy_async();
+      mbar_arrive(&empty[s]);
+    }
+  }
+  named_sync(2, kThreadsD);  // the producer is done issuing
+  if (dead) {
+    const int issued = *s_issued;  // copies that this warp did not see land, at most one per stage
+    for (int i = i_dead; i < issued; ++i)
+      (void)mbar_wait_bounded(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u);
+  }
+  allow_successor();
+  end_item(c);
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream) {
+  using C = DCfg<D>;
+  int unused = 0;
+  cudaError_t e = per_device_setup(a.device, &unused, [](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(paged_decode_kernel<T, D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::bytes(kMaxRequests));
+  });
+  if (e != cudaSuccess) return e;
+  const long rows = ((long)a.num_pages * a.Hkv) << a.page_shift;
+  const int box = a.page_shift < 6 ? 1 << a.page_shift : kTileD;
+  CUtensorMap tk, tv;
+  if (!encode_bf16_map(&tk, a.k, rows, D, box) || !encode_bf16_map(&tv, a.v, rows, D, box))
+    return cudaErrorInvalidValue;
+  const int grid = a.num_sms < kMaxGrid ? a.num_sms : kMaxGrid;
+  e = launch_pdl(paged_decode_kernel<T, D>, dim3(grid), dim3(kThreadsD), C::bytes(a.B), stream, tk,
+                 tv, a, scale_log2);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+long paged_decode_partial_bytes(int D) { return (long)kMaxGrid * 2 * kDecodeRows * (D + 2) * 4; }
+
+cudaError_t launch_paged_decode(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream) {
+  if (a.dtype == 0)
+    return a.D == 128 ? launch_t<__nv_bfloat16, 128>(a, scale_log2, stream)
+                      : launch_t<__nv_bfloat16, 64>(a, scale_log2, stream);
+  return a.D == 128 ? launch_t<__half, 128>(a, scale_log2, stream)
+                    : launch_t<__half, 64>(a, scale_log2, stream);
+}
+
+}  // namespace kivi

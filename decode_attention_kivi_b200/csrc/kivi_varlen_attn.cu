@@ -10,9 +10,7 @@
 
 #include <cmath>
 
-#include "kivi_paged.h"
-#include "kivi_ptx.cuh"
-#include "kivi_request.cuh"
+#include "kivi_varlen.cuh"
 
 namespace kivi {
 namespace {
@@ -36,7 +34,7 @@ __device__ __forceinline__ __half from_float<__half>(float x) {
 // over the keys with the running maximum and sum.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-varlen_attention_simple_kernel(VarlenAttnArgs a) {
+varlen_attention_simple_kernel(VarlenAttnArgs a, bool skip_short) {
   const long w = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (w >= (long)a.T * a.Hq) return;
@@ -50,7 +48,7 @@ varlen_attention_simple_kernel(VarlenAttnArgs a) {
     if (bad && lane == 0) atomicOr(a.status, kPagedBadLength);
     if (t >= r.q0 && t < r.q0 + r.n) break;
   }
-  if (b == a.B) return;
+  if (b == a.B || (skip_short && is_short(r.n, a.Hq / a.Hkv))) return;
   const T* q = static_cast<const T*>(a.q) + t * a.q_stride + (long)h * D;
   constexpr int E = D / 32;
   float qv[E], acc[E];
@@ -97,19 +95,28 @@ varlen_attention_simple_kernel(VarlenAttnArgs a) {
 }
 
 template <typename T>
-cudaError_t launch_simple(const VarlenAttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_simple(const VarlenAttnArgs& a, bool skip_short, cudaStream_t stream) {
   const long warps = (long)a.T * a.Hq, blocks = (warps + 3) / 4;
   if (a.D == 128)
-    varlen_attention_simple_kernel<T, 128><<<(unsigned)blocks, 128, 0, stream>>>(a);
+    varlen_attention_simple_kernel<T, 128><<<(unsigned)blocks, 128, 0, stream>>>(a, skip_short);
   else
-    varlen_attention_simple_kernel<T, 64><<<(unsigned)blocks, 128, 0, stream>>>(a);
+    varlen_attention_simple_kernel<T, 64><<<(unsigned)blocks, 128, 0, stream>>>(a, skip_short);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+long varlen_partial_bytes(int D) { return paged_decode_partial_bytes(D); }
+
 cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream) {
-  return a.dtype == 0 ? launch_simple<__nv_bfloat16>(a, stream) : launch_simple<__half>(a, stream);
+  const float scale = a.sm_scale > 0.f ? a.sm_scale : 1.f / std::sqrt((float)a.D);
+  const bool decode = a.table != nullptr && is_short(1, a.Hq / a.Hkv);
+  if (decode) {
+    const cudaError_t e = launch_paged_decode(a, scale * kLog2eV, stream);
+    if (e != cudaSuccess || is_short(a.max_new, a.Hq / a.Hkv)) return e;
+  }
+  return a.dtype == 0 ? launch_simple<__nv_bfloat16>(a, decode, stream)
+                      : launch_simple<__half>(a, decode, stream);
 }
 
 }  // namespace kivi

@@ -447,9 +447,10 @@ kivi_status kivi_paged_append(const void* k_new, int64_t k_stride, const void* v
                               int32_t num_kv_heads, int32_t head_dim, uint32_t* status,
                               void* stream);
 
-/* Workspace bytes of the two attention calls below: a status header (256 B, the
+/* Workspace bytes of the two attention calls below: a header of 1 KB (the status
  * word first) and the partial results of rows whose keys are split.  Host only.
- * The header must be zero-filled before first use; calls that share a workspace
+ * The header must be zero-filled before first use and is zero again after each
+ * call, except for the status word; calls that share a workspace
  * must not overlap on the GPU (two captured graphs that may run side by side need
  * one each).  Errors: INVALID_ARG, UNSUPPORTED (head_dim, head ratio). */
 kivi_status kivi_attention_workspace_bytes(int32_t num_kv_heads, int32_t num_q_heads,
