@@ -11,11 +11,12 @@ namespace kivi {
 constexpr int kMaxRequests = 4096;   // requests of one call (their prefix sums sit in shared memory)
 constexpr int kMinPage = 16, kMaxPage = 256;
 
-// Workspace of the attention calls: the status word, tickets from byte 64 on, and from
-// kPagedHeader on the partials of at most kMaxGrid CTAs.
+// Workspace of the attention calls: the status word, tickets (eight per CTA) from byte 64 on,
+// and from kPagedHeader on the partials of at most kMaxGrid CTAs.
 constexpr int kMaxGrid = 160;
-constexpr int kPagedHeader = 1024;
-static_assert(64 + 4 * kMaxGrid <= kPagedHeader, "tickets");
+constexpr int kTickets = 8;
+constexpr int kPagedHeader = 8192;
+static_assert(64 + 4 * kTickets * kMaxGrid <= kPagedHeader, "tickets");
 
 // Bits of a status word (a call ORs them in; KIVI_PAGED_* in kivi.h).
 constexpr uint32_t kPagedTimeout = 1u;     // a bounded wait ran out
@@ -65,7 +66,7 @@ struct VarlenAttnArgs {
   const int* kv_lengths;  // [B], paged only
   const int* table;       // [B][width], paged only
   uint32_t* status;       // workspace header: the status word,
-  int* tickets;           // then one ticket per CTA, zero between calls
+  int* tickets;           // then the tickets, zero between calls
   uint8_t* partials;      // the rest of the workspace
   long q_stride, k_stride, v_stride, out_stride;  // elements between rows (k, v: packed only)
   int dtype;              // 0 bf16, 1 fp16

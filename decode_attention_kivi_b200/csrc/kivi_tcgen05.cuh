@@ -34,6 +34,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major)
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// As idesc_bf16, with fp16 A and B where `bf16` is false (A and B have one type).
+__host__ __device__ constexpr uint32_t idesc_16bit(int M, int N, bool b_mn_major, bool bf16) {
+  return idesc_bf16(M, N, b_mn_major) & ~(bf16 ? 0u : (1u << 7) | (1u << 10));
+}
+
 // Executed by one whole warp: allocates `ncols` TMEM columns (a power of two,
 // >= 32) and writes the base address to `slot` in shared memory.
 __device__ __forceinline__ void alloc(uint32_t* slot, uint32_t ncols) {
@@ -64,6 +69,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// The same with A in TMEM: 16-bit pairs, one per 32-bit column, row i in lane i.
+__device__ __forceinline__ void mma_16bit_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                                 uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
 
@@ -172,10 +187,7 @@ __device__ __forceinline__ void ld_x128(uint32_t taddr, float (&v)[128]) {
 
 // Warp-collective store of 32 consecutive fp32 columns per lane (see ld_x32);
 // complete after wait_st.
-__device__ __forceinline__ void st_x32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
       "%1,%2,%3,%4,%5,%6,%7,%8,"
@@ -192,6 +204,12 @@ __device__ __forceinline__ void st_x32(uint32_t taddr, const float (&v)[32]) {
       "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+__device__ __forceinline__ void st_x32(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  st_x32(taddr, r);
 }
 __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

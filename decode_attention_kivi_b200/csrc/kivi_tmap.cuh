@@ -25,12 +25,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // [rows][cols] bf16 at `base` (16-byte aligned, cols * 2 a multiple of 16),
 // copied in boxes of 64 columns (128 bytes, the swizzle span) x box_rows rows
 // with the 128-byte swizzle; rows past the end read as zero.
-inline bool encode_bf16_map(CUtensorMap* map, const void* base, long rows, int cols,
-                            int box_rows) {
+// `row_stride`: elements between rows (0: cols), a multiple of 8.
+inline bool encode_bf16_map(CUtensorMap* map, const void* base, long rows, int cols, int box_rows,
+                            long row_stride = 0) {
   const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint64_t strides[1] = {(cuuint64_t)(row_stride ? row_stride : cols) * 2};
   const cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,

@@ -1,122 +1,755 @@
 // kivi_varlen_attn.cu - causal attention of packed rows of different requests,
 // over the rows' own keys (whole prompts) or over a paged 16-bit cache (chunks
-// of new tokens, single tokens).
+// of new tokens), on the fifth-generation tensor cores.
 //
 //   out[t][h] = sum_j softmax_j(sm_scale <q[t][h], k_j[h / g]>) v_j[h / g]
 //
 // over the keys j that row t of its request sees.  A row without keys is 0.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+//
+// The n new rows and g query heads of a (request, kv head) give n * g tile rows
+// (token i, head h at row i * g + h), so that short chunks fill a tile and all
+// heads of a group share the keys' copies.  An item is 256 of them, two halves
+// of 128 (the TMEM lanes), with the tiles of 128 keys that they see: 4 * 128 *
+// 256 * D FLOPs against 2 * 128 * D values copied per tile, 256 FLOPs per byte,
+// so long chunks are bound by the tensor cores and, equally, by the 128 * 256
+// exponentials of a tile (16 per SM and cycle: 2048 cycles, as long as its
+// products take).
+// The tiles of all items, in order, are cut into one contiguous range per CTA,
+// equal to within a tile whatever the lengths are; every CTA forms the prefix
+// sums that this needs from the device arrays.
+//
+// Twelve warps (two idle), one CTA per SM:
+//   warp 9 (producer)  2D tensor copies of K and V tiles into a ring of four
+//                      slots, page by page (a box of min(page, 128) rows x 64
+//                      channels per lane) or in one piece;
+//   warp 8 (MMA)       one lane issues S_i = Q_i K^T (M = N = 128) for half i
+//                      into its score columns and O_i += P_i V, P_i read from
+//                      TMEM, where it lies over the first half of S_i; the two
+//                      halves alternate, so that the tensor cores work on one
+//                      while the other is in its softmax.  Only the 16-key steps
+//                      with keys that the half sees are issued;
+//   warps 0-7          one row per thread (its TMEM lane): the row of S from
+//                      TMEM, the mask where the tile needs one, the online
+//                      softmax in base 2, P back to TMEM.  O is rescaled only
+//                      when a row's maximum grew by more than 2^8 (up to then
+//                      the stale maximum is kept: weights stay below 2^8 and
+//                      O / l is unchanged).  The next item's Q rows are fetched
+//                      during the last tile of this one.
+// An item that lies in several CTAs leaves a partial (m, l, O in fp32) per CTA,
+// joined in CTA order, so results do not depend on the order of arrival: by the
+// warp that arrives last (a ticket per CTA and warp), or, where few items are
+// cut into many pieces, by a second kernel over all SMs.
+// TMEM: S_0 and S_1 at columns 0 and 128, O_0 at 256, O_1 behind it.
+// Every wait is bounded; a wait that runs out sets the status word, and what was
+// issued is drained before TMEM is released.
 #include <cmath>
 
+#include "kivi_launch.cuh"
+#include "kivi_tcgen05.cuh"
 #include "kivi_varlen.cuh"
 
 namespace kivi {
 namespace {
 
 constexpr float kLog2eV = 1.4426950408889634f;
+constexpr int kHalf = 128;             // rows of a half = TMEM lanes
+constexpr int kTileV = 128;            // keys per tile
+constexpr int kSoftWarpsV = 8;
+constexpr int kMmaWarpV = kSoftWarpsV, kProducerWarpV = kSoftWarpsV + 1;
+constexpr int kThreadsV = (kSoftWarpsV + 4) * 32;  // three warpgroups; two warps of the last idle
+// Registers per thread at launch, and after the softmax warpgroups took what the third gave up.
+constexpr int kRegsV = 168, kRegsSoft = 208, kRegsRest = 88;
+static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegsV, "a larger sum would wait forever");
+constexpr int kSlabV = 128 * 128;      // 128 rows of 64 channels
+constexpr int kSlots = 4;              // K and V tiles in flight
+constexpr uint32_t kTmemColsV = 512;
+constexpr float kSlackV = 8.f;         // log2 growth of a row maximum before O is rescaled
+constexpr int kMinTilesV = 4;          // tiles per CTA at least
+// one item cut into pieces: what the joining kernel needs
+struct Cut {
+  int count, q0, kvh, row0, rows, pad[3];
+};
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) {
-  return __float2half_rn(x);
-}
-
-// One warp per (row, query head): lane i holds channels i, i + 32, ...; one pass
-// over the keys with the running maximum and sum.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-varlen_attention_simple_kernel(VarlenAttnArgs a, bool skip_short) {
-  const long w = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= (long)a.T * a.Hq) return;
-  const int t = (int)(w / a.Hq), h = (int)(w % a.Hq), kvh = h / (a.Hq / a.Hkv);
-  // the request of row t
-  Request r{};
-  int b = 0;
-  for (; b < a.B; ++b) {
-    bool bad = false;
-    r = load_request(a, b, &bad);
-    if (bad && lane == 0) atomicOr(a.status, kPagedBadLength);
-    if (t >= r.q0 && t < r.q0 + r.n) break;
+template <int D>
+struct VCfg {
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kTileBytes = kSlabs * kSlabV;
+  static constexpr int kOffRing = 2 * kTileBytes;  // after the two halves of Q
+  static constexpr int kOffBars = kOffRing + kSlots * kTileBytes;
+  static constexpr int kOffPrefix = kOffBars + 256;
+  static constexpr int kWarpState = 32 * (D + 2);  // O [D/4][32] float4, m [32], l [32]
+  static constexpr int kState = kSoftWarpsV * kWarpState;
+  static constexpr uint32_t kColO = 2 * kTileV;
+  // more than half of the SM's shared memory: one CTA per SM, which holds all of TMEM
+  static constexpr int bytes(int B) {
+    const int n = kOffPrefix + 4 * (B + 1) + 1024;
+    return n > 120 * 1024 ? n : 120 * 1024;
   }
-  if (b == a.B || (skip_short && is_short(r.n, a.Hq / a.Hkv))) return;
-  const T* q = static_cast<const T*>(a.q) + t * a.q_stride + (long)h * D;
-  constexpr int E = D / 32;
-  float qv[E], acc[E];
+  static_assert(bytes(kMaxRequests) <= 227 * 1024, "shared-memory plan");
+  static_assert(kColO + 2 * D <= kTmemColsV, "TMEM plan");
+};
+
+// Tiles that the half of rows row0 .. row0 + 127 of an item sees; at least one where it has rows.
+__device__ __forceinline__ int half_tiles(const Request& r, int rows, int row0, int hpk) {
+  if (row0 >= rows) return 0;
+  const int kmax = min(last_key(r, (min(row0 + kHalf, rows) - 1) / hpk), r.L - 1);
+  return kmax < 0 ? 1 : kmax / kTileV + 1;
+}
+__device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, int hpk) {
+  return max(half_tiles(r, rows, tt * 2 * kHalf, hpk),
+             half_tiles(r, rows, tt * 2 * kHalf + kHalf, hpk));
+}
+
+struct Ranges {
+  int n, q, rem;  // CTAs with work; total = n * q + rem
+  __device__ __forceinline__ int lo(int c) const { return c * q + min(c, rem); }
+  __device__ __forceinline__ int cta_of(int t) const {
+    const int big = rem * (q + 1);
+    return t < big ? t / (q + 1) : rem + (t - big) / q;
+  }
+};
+
+// A CTA's piece of an item: tiles j0 .. j1 - 1 of nt, half i active below e[i].
+struct Piece {
+  int t;  // tiles before this one in the whole call
+  int b, kvh, tt, rows, j0, j1, nt, e[2];
+  Request r;
+};
+
+// The rows' joined output from `count` partials, in order; src(w) is a warp's state.
+template <typename T, int D, int C4, typename Src>
+__device__ __forceinline__ void join_rows(int count, Src src, int lane, int c4_0, bool real, T* dst) {
+  float M = -INFINITY;
+  for (int w = 0; w < count; ++w) M = fmaxf(M, __ldcg(src(w) + 32 * D + lane));
+  float L = 0.f, acc[4 * C4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_float(q[lane + 32 * e]);
-    acc[e] = 0.f;
+  for (int i = 0; i < 4 * C4; ++i) acc[i] = 0.f;
+  for (int w = 0; w < count; ++w) {
+    const float* s = src(w);
+    const float mw = __ldcg(s + 32 * D + lane);
+    if (mw == -INFINITY) continue;  // nothing seen there, its O is not written
+    const float f = fast_exp2(mw - M);
+    L += f * __ldcg(s + 32 * (D + 1) + lane);
+#pragma unroll
+    for (int c = 0; c < C4; ++c) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (c4_0 + c) * 32 + lane);
+      acc[4 * c] += f * v.x;
+      acc[4 * c + 1] += f * v.y;
+      acc[4 * c + 2] += f * v.z;
+      acc[4 * c + 3] += f * v.w;
+    }
   }
-  const float sl2 = (a.sm_scale > 0.f ? a.sm_scale : rsqrtf((float)D)) * kLog2eV;
-  float m = -INFINITY, l = 0.f;
-  const int last = min(last_key(r, t - r.q0), r.L - 1);
-  for (int j = 0; j <= last; ++j) {
-    const T *k, *v;
-    if (a.table == nullptr) {
-      k = static_cast<const T*>(a.k) + (r.q0 + j) * a.k_stride + (long)kvh * D;
-      v = static_cast<const T*>(a.v) + (r.q0 + j) * a.v_stride + (long)kvh * D;
-    } else {
-      const int page = a.table[(long)b * a.width + (j >> a.page_shift)];
-      if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) atomicOr(a.status, kPagedBadPage);
-        k = v = nullptr;
-      } else {
-        const long row = (((long)page * a.Hkv + kvh) << a.page_shift) +
-                         (j & ((1 << a.page_shift) - 1));
-        k = static_cast<const T*>(a.k) + row * D;
-        v = static_cast<const T*>(a.v) + row * D;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  if (real)
+#pragma unroll
+    for (int c = 0; c < C4; c += 2)
+      *reinterpret_cast<uint4*>(dst + 4 * (c4_0 + c)) =
+          make_uint4(Elem<T>::pack(acc[4 * c] * inv, acc[4 * c + 1] * inv),
+                     Elem<T>::pack(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv),
+                     Elem<T>::pack(acc[4 * c + 4] * inv, acc[4 * c + 5] * inv),
+                     Elem<T>::pack(acc[4 * c + 6] * inv, acc[4 * c + 7] * inv));
+}
+
+template <int D>
+__device__ __forceinline__ float* partial_of(const VarlenAttnArgs& a, int cta, int which) {
+  return reinterpret_cast<float*>(a.partials + kMaxGrid * sizeof(Cut)) +
+         ((long)cta * 2 + which) * VCfg<D>::kState;
+}
+
+template <typename T, int D, bool PAGED>
+__global__ void __launch_bounds__(kThreadsV, 1)
+varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, VarlenAttnArgs a, float scale_log2,
+                        bool skip_short, bool join_here) {
+  using C = VCfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [kSlots]
+  uint64_t* empty = full + kSlots;
+  uint64_t* q_full = empty + kSlots;  // [2] each, by half
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_done = p_full + 2;
+  uint64_t* drained = o_done + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, kvh, tt, j of the CTA's first tile
+  int* s_sum = s_start + 4;                           // [kThreadsV / 32]
+  int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hpk = a.Hq / a.Hkv;
+
+  if (threadIdx.x == 0) {
+    *s_abort = 0;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], kHalf);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kHalf);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(drained, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarpV) {
+    tc::alloc(s_tmem, kTmemColsV);
+    tc::relinquish();
+  }
+  wait_for_predecessor();
+
+  // ---- prefix sums of the requests' tiles ----
+  long long base = 0;
+  bool fits = true;
+  for (int b0 = 0; b0 < a.B; b0 += kThreadsV) {
+    const int b = b0 + threadIdx.x;
+    Request r{0, 0, 0};
+    if (b < a.B) {
+      bool bad = false;
+      r = load_request(a, b, &bad);
+      if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
+      if (skip_short && is_short(r.n, hpk)) r.n = 0;
+    }
+    const int rows = r.n * hpk, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
+    long long v = 0;
+    if (items <= 4)
+      for (int tt = 0; tt < items; ++tt) v += item_tiles(r, rows, tt, hpk);
+    // requests of many items: the warp's lanes share them
+    for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
+      const int from = __ffs(left) - 1;
+      const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
+      const int rrows = rr.n * hpk;
+      long long sum = 0;
+      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_tiles(rr, rrows, tt, hpk);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == from) v = sum;
+    }
+    v *= a.Hkv;
+    long long inc = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    // a warp's sum that an int does not hold makes the call's total too large
+    fits = fits && inc <= INT32_MAX;
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = (int)inc;
+    fits = __syncthreads_and(fits);
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreadsV / 32; ++w) {
+      if (w < warp) before += s_sum[w];
+      all += s_sum[w];
+    }
+    if (b < a.B) prefix[b] = (int)(base + before + inc - v);
+    base += all;
+    fits = fits && base <= INT32_MAX;
+    if (!fits) break;
+  }
+  if (threadIdx.x == 0) {
+    prefix[a.B] = (int)base;
+    if (!fits && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int cta = blockIdx.x;
+  Ranges sp{0, 0, 0};
+  int t_begin = 0, t_end = 0;
+  if (fits && base > 0) {
+    sp.n = min((int)gridDim.x, (int)((base + kMinTilesV - 1) / kMinTilesV));
+    sp.q = (int)base / sp.n;
+    sp.rem = (int)base - sp.n * sp.q;
+    if (cta < sp.n) {
+      t_begin = sp.lo(cta);
+      t_end = sp.lo(cta + 1);
+    }
+  }
+  if (warp == 0 && t_begin < t_end) {
+    int lo = 0, hi = a.B;  // largest b with prefix[b] <= t_begin
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= t_begin) lo = mid;
+      else hi = mid;
+    }
+    bool bad;
+    const Request r = load_request(a, lo, &bad);
+    const int rows = r.n * hpk, per_head = (prefix[lo + 1] - prefix[lo]) / a.Hkv;
+    const int kvh = (t_begin - prefix[lo]) / per_head;
+    int x = t_begin - prefix[lo] - kvh * per_head;  // tiles to pass within the head
+    for (int t0 = 0;; t0 += 32) {
+      const int v = item_tiles(r, rows, t0 + lane, hpk);
+      int inc = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, inc > x);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          s_start[0] = lo;
+          s_start[1] = kvh;
+          s_start[2] = t0 + lane;
+          s_start[3] = x - (inc - v);
+        }
+        break;
+      }
+      x -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  __syncthreads();
+
+  auto set_item = [&](Piece& p, int j0) {
+    const int row0 = p.tt * 2 * kHalf;
+    p.e[0] = half_tiles(p.r, p.rows, row0, hpk);
+    p.e[1] = half_tiles(p.r, p.rows, row0 + kHalf, hpk);
+    p.nt = max(p.e[0], p.e[1]);
+    p.j0 = j0;
+    p.j1 = min(p.nt, j0 + (t_end - p.t));
+    p.e[0] = min(p.e[0], p.j1);
+    p.e[1] = min(p.e[1], p.j1);
+  };
+  auto set_request = [&](Piece& p, int b) {
+    bool bad;
+    p.b = b;
+    p.r = load_request(a, b, &bad);
+    p.rows = p.r.n * hpk;
+  };
+  auto first_piece = [&]() {
+    Piece p;
+    p.t = t_begin;
+    if (t_begin < t_end) {
+      set_request(p, s_start[0]);
+      p.kvh = s_start[1];
+      p.tt = s_start[2];
+      set_item(p, s_start[3]);
+    }
+    return p;
+  };
+  // the piece after p; it is there if its t < t_end
+  auto next_piece = [&](Piece& p) {
+    p.t += p.j1 - p.j0;
+    if (p.t >= t_end) return;
+    if (++p.tt * 2 * kHalf >= p.rows) {
+      p.tt = 0;
+      if (++p.kvh == a.Hkv) {
+        p.kvh = 0;
+        int b = p.b + 1;
+        while (prefix[b + 1] == prefix[b]) ++b;
+        set_request(p, b);
       }
     }
-    float s = 0.f;
+    set_item(p, 0);
+  };
+  auto fail = [&]() {
+    *s_abort = 1;
+    atomicOr(a.status, kPagedTimeout);
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    const bool w = mbar_wait_bounded(bar, parity);
+    return __all_sync(0xffffffffu, w && *s_abort == 0);
+  };
+
+  if (warp < kSoftWarpsV) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ---- softmax: half `hf`, thread r owns its row r (TMEM lane r) ----
+    const int hf = warp >> 2, r = threadIdx.x & (kHalf - 1);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t col_s = lanes + hf * kTileV, col_o = lanes + C::kColO + hf * D;
+    unsigned char* qs = smem + hf * C::kTileBytes;
+    // starts the copies of the half's Q rows (a row is 2 D bytes, D / 8 lanes to a row)
+    auto fetch_q = [&](const Piece& p) {
+      const int row = p.tt * 2 * kHalf + hf * kHalf + r, i = row / hpk;
+      const bool real = row < p.rows;
+      const long off = real ? (p.r.q0 + i) * a.q_stride + (long)(p.kvh * hpk + row - i * hpk) * D : -1;
+      constexpr int kPer = D / 8, kStep = 32 / kPer;  // lanes per row, rows per step
+      const int c = lane % kPer, first = (warp & 3) * 32;
+#pragma unroll 4
+      for (int x = 0; x < 32; x += kStep) {
+        const int rr = x + lane / kPer;
+        const long o = __shfl_sync(0xffffffffu, off, rr);
+        const int row_s = first + rr;
+        const uint32_t dst = smem_addr(qs + (c >> 3) * kSlabV + row_s * 128 +
+                                       (((c & 7) ^ (row_s & 7)) << 4));
+        const T* src = static_cast<const T*>(a.q) + (o < 0 ? 0 : o + 8 * c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                     "r"(o < 0 ? 0 : 16)
+                     : "memory");
+      }
+    };
+    auto q_here = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async();  // Q is read by the tensor cores
+      mbar_arrive(&q_full[hf]);
+    };
+    uint32_t ns = 0, no = 0;
+    bool ok = true;
+    Cut cut{0, 0, 0, 0, 0, {0, 0, 0}};
+    Piece p = first_piece();
+    if (p.t < t_end && p.e[hf] > p.j0) {
+      fetch_q(p);
+      q_here();
+    }
+    while (ok && p.t < t_end) {
+      Piece nx = p;
+      next_piece(nx);
+      const bool more = nx.t < t_end && nx.e[hf] > nx.j0;
+      const bool active = p.e[hf] > p.j0;
+      const int row = p.tt * 2 * kHalf + hf * kHalf + r, qi = row / hpk;
+      const bool real = row < p.rows;
+      const int last = real ? min(last_key(p.r, qi), p.r.L - 1) : -1;
+      // tiles that end behind this key need the mask
+      const int clear = min(last_key(p.r, (row - r) / hpk), p.r.L - 1);
+      float m = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
+      for (int j = p.j0; j < p.e[hf]; ++j) {
+        if (!(ok = wait_warp(&s_full[hf], ns++ & 1u))) break;
+        tc::fence_after();
+        if (more && j + 1 == p.e[hf]) fetch_q(nx);  // this item's scores are done with Q
+        float s[kTileV];
+        tc::ld_x128(col_s, s);
+        const int key0 = j * kTileV;
+        if (key0 + kTileV - 1 > clear) {
+          const int lim = last - key0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s += k ? qv[e] * to_float(k[lane + 32 * e]) : 0.f;
+          for (int c = 0; c < kTileV; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+        }
+        float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= sl2;
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * al + p;
+        for (int c = 4; c < kTileV; c += 8)
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + (v ? p * to_float(v[lane + 32 * e]) : 0.f);
+          for (int x = 0; x < 4; ++x)
+            mx4[x] = c + 4 + x < kTileV ? fmax3(mx4[x], s[c + x], s[c + 4 + x]) : fmaxf(mx4[x], s[c + x]);
+        const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale_log2;
+        const bool grow = mx > m + kSlackV;  // always where m = -inf and a key is seen
+        const float mn = grow ? mx : m, mu = mn == -INFINITY ? 0.f : mn;
+        const float al = fast_exp2(m - mu);  // 1 where kept, 0 at a row's first keys
+        m = mn;
+        // S(j) came after P V of tile j - 1 on the tensor cores: O is complete up to it
+        if (j > p.j0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tc::ld_x32(col_o + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= grow ? al : 1.f;
+            tc::st_x32(col_o + c0, o);
+          }
+        }
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-mu, -mu);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float2 x = fma2(make_float2(s[64 * q + 2 * c], s[64 * q + 2 * c + 1]), sc, nm);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            sum[c & 1] = add2(sum[c & 1], x);
+            pk[c] = Elem<T>::pack(x.x, x.y);
+          }
+          tc::st_x32(col_s + 32 * q, pk);
+        }
+        l = l * (grow ? al : 1.f) + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&p_full[hf]);
+      }
+      if (!ok) break;
+      if (!active && more) fetch_q(nx);
+      if (more) q_here();
+      if (active) {
+        if (!(ok = wait_warp(&o_done[hf], no++ & 1u))) break;
+        tc::fence_after();
+      }
+      T* dst = static_cast<T*>(a.out) + (p.r.q0 + (real ? qi : 0)) * a.out_stride +
+               (long)(p.kvh * hpk + (real ? row - qi * hpk : 0)) * D;
+      if (p.j0 == 0 && p.j1 == p.nt) {
+        if (active) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tc::ld_x32(col_o + c0, o);
+            if (real)
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)  // no product was made where no key is seen
+                  w[x] = l > 0.f ? Elem<T>::pack(o[i + 2 * x] * inv, o[i + 2 * x + 1] * inv) : 0u;
+                *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+          }
+        }
+      } else if (p.tt * 2 * kHalf + (warp >> 2) * kHalf + (warp & 3) * 32 < p.rows) {
+        // slot 0: the item this CTA begins in the middle of; slot 1: the one it leaves unfinished
+        float* part = partial_of<D>(a, cta, p.j0 > 0 ? 0 : 1) + warp * C::kWarpState;
+        if (active) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tc::ld_x32(col_o + c0, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(part)[(c0 / 4 + i) * 32 + lane] =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        part[32 * D + lane] = m;
+        part[32 * (D + 1) + lane] = l;
+        const int first = p.t - p.j0, c0 = sp.cta_of(first), c1 = sp.cta_of(first + p.nt - 1);
+        if (join_here) {
+          __threadfence();
+          __syncwarp();
+          int* ticket = a.tickets + c0 * kTickets + warp;
+          int arrived = 0;
+          if (lane == 0) arrived = atomicAdd(ticket, 1);
+          if (__shfl_sync(0xffffffffu, arrived, 0) == c1 - c0) {
+            __threadfence();
+            join_rows<T, D, D / 4>(
+                c1 - c0 + 1,
+                [&](int w) { return partial_of<D>(a, c0 + w, w == 0 ? 1 : 0) + warp * C::kWarpState; },
+                lane, 0, real, dst);
+            if (lane == 0) *ticket = 0;  // ready for the next call
+          }
+        } else if (p.j0 == 0) {
+          cut = Cut{c1 - c0 + 1, p.r.q0, p.kvh, p.tt * 2 * kHalf, p.rows, {0, 0, 0}};
+        }
+      }
+      p = nx;
+    }
+    if (!ok) fail();
+    if (!join_here && threadIdx.x == 0) reinterpret_cast<Cut*>(a.partials)[cta] = cut;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kProducerWarpV) {
+      // ---- producer: tiles u = 2 s (K) and 2 s + 1 (V) of the CTA's step s, slot u mod 4 ----
+      const int box = PAGED ? min(1 << a.page_shift, kTileV) : kTileV;
+      const int boxes = kTileV / box * C::kSlabs;  // of a tile, one per lane (at most 16)
+      const int slab = lane % C::kSlabs, part = lane / C::kSlabs;
+      const int outside = PAGED ? (a.num_pages * a.Hkv) << a.page_shift : 0;  // rows of zeros
+      int u = 0;
+      bool ok = true;
+      for (Piece p = first_piece(); ok && p.t < t_end; next_piece(p)) {
+        for (int j = p.j0; ok && j < p.j1; ++j) {
+          const int key = j * kTileV + part * box;
+          const bool mine = lane < boxes && key < p.r.L;
+          int x = 64 * slab, y = 0;
+          if (PAGED) {
+            y = outside;
+            if (mine) {
+              const int id = a.table[(long)p.b * a.width + (key >> a.page_shift)];
+              if (id >= 0 && id < a.num_pages)
+                y = ((id * a.Hkv + p.kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+              else
+                atomicOr(a.status, kPagedBadPage);
+            }
+          } else {
+            x += p.kvh * D;
+            y = p.r.q0 + key;
+          }
+          const int n = __popc(__ballot_sync(0xffffffffu, mine));
+          for (int v = 0; v < 2; ++v, ++u) {
+            const int s = u % kSlots;
+            if (u >= kSlots && !wait_warp(&empty[s], (uint32_t)(u / kSlots - 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            unsigned char* dst = smem + C::kOffRing + s * C::kTileBytes;
+            if (lane == 0) mbar_expect_tx(&full[s], n * box * 128);
+            __syncwarp();
+            if (mine) tma_load_2d(dst + slab * kSlabV + part * box * 128, v ? &tv : &tk, x, y, &full[s]);
+          }
+        }
+      }
+      if (!ok) fail();
+      // every copy issued lands before the CTA may exit
+      for (int i = max(u - kSlots, 0); i < u; ++i)
+        if (!mbar_wait_bounded(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u)) fail();
+    } else if (warp == kMmaWarpV) {
+      // ---- MMA ----
+      constexpr bool kBf16 = sizeof(T) == 2 && Elem<T>::kBf16;
+      constexpr uint32_t id_s = tc::idesc_16bit(kHalf, kTileV, false, kBf16);
+      constexpr uint32_t id_o = tc::idesc_16bit(kHalf, D, true, kBf16);
+      const uint32_t q_base = smem_addr(smem), ring = smem_addr(smem + C::kOffRing);
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      int u = 0;  // tiles consumed, as the producer counts them
+      bool ok = true;
+      auto wait_tile = [&](int i) { return wait_warp(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u); };
+      auto scores = [&](int i, int tile) {
+        if (lane == 0) {
+  #pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s >> 2) * kSlabV + (s & 3) * 32;
+            tc::mma_bf16(tmem + i * kTileV, tc::desc_sw128(q_base + i * C::kTileBytes + off, 16, 1024),
+                         tc::desc_sw128(ring + (tile % kSlots) * C::kTileBytes + off, 16, 1024), id_s,
+                         s > 0);
+          }
+          tc::commit(&s_full[i]);
+        }
+      };
+      for (Piece p = first_piece(); ok && p.t < t_end; next_piece(p)) {
+        const int row0 = p.tt * 2 * kHalf;
+        int seen[2];  // keys that some row of the half sees
+        for (int i = 0; i < 2; ++i)
+          seen[i] = min(last_key(p.r, (min(row0 + (i + 1) * kHalf, p.rows) - 1) / hpk) + 1, p.r.L);
+        ok = wait_tile(u);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (p.e[i] <= p.j0) continue;
+          ok = wait_warp(&q_full[i], nq[i]++ & 1u);
+          if (!ok) break;
+          tc::fence_after();
+          scores(i, u);
+        }
+        if (ok && lane == 0) tc::commit(&empty[u % kSlots]);
+        for (int j = p.j0; ok && j < p.j1; ++j) {
+          const int tile_v = u + 1, tile_k = u + 2;
+          u += 2;
+          if (!(ok = wait_tile(tile_v))) break;
+          const uint32_t vb = ring + (tile_v % kSlots) * C::kTileBytes;
+          const int nv = min(kTileV, p.r.L - j * kTileV);
+          if (nv > 0 && (nv & 15)) {  // rows behind the last key: a weight of 0 times NaN
+            unsigned char* vs = smem + C::kOffRing + (tile_v % kSlots) * C::kTileBytes;
+            for (int x = lane; x < (16 - (nv & 15)) * C::kSlabs * 8; x += 32) {
+              const int row = nv + x / (C::kSlabs * 8), rest = x % (C::kSlabs * 8);
+              *reinterpret_cast<uint4*>(vs + (rest / 8) * kSlabV + row * 128 + 16 * (rest % 8)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+          const int e_max = max(p.e[0], p.e[1]);
+          for (int i = 0; i < 2; ++i) {
+            if (j < p.e[i]) {
+              if (!(ok = wait_warp(&p_full[i], np[i]++ & 1u))) break;
+              tc::fence_after();
+              if (lane == 0) {
+                const int steps = (min(kTileV, seen[i] - j * kTileV) + 15) >> 4;
+                for (int s = 0; s < steps; ++s)
+                  tc::mma_16bit_tmem_a(tmem + C::kColO + i * D, tmem + i * kTileV + s * 8,
+                                       tc::desc_sw128(vb + s * 16 * 128, kSlabV, 1024), id_o,
+                                       j > p.j0 || s > 0);
+                if (j + 1 == p.e[i]) tc::commit(&o_done[i]);
+              }
+            }
+            if (i == 1 && lane == 0) tc::commit(&empty[tile_v % kSlots]);
+            if (j + 1 < p.e[i]) {
+              if (!(ok = wait_tile(tile_k))) break;
+              tc::fence_after();
+              scores(i, tile_k);
+            }
+          }
+          if (ok && j + 1 < e_max && lane == 0) tc::commit(&empty[tile_k % kSlots]);
+        }
+      }
+      if (!ok) fail();
+      // all that was issued has completed before TMEM is released
+      if (lane == 0) {
+        tc::commit(drained);
+        if (!mbar_wait_bounded(drained, 0)) fail();
+      }
+      __syncwarp();
+    }
   }
-  T* out = static_cast<T*>(a.out) + t * a.out_stride + (long)h * D;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane + 32 * e] = from_float<T>(last < 0 ? 0.f : acc[e] / l);
+  allow_successor();
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarpV) {
+    tc::fence_after();
+    tc::dealloc(tmem, kTmemColsV);
+  }
+}
+
+// The join of cut items: block (c, w) takes the 32 rows of warp w of the item that CTA c leaves
+// unfinished, D / 32 float4 columns per warp.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+varlen_join_kernel(VarlenAttnArgs a) {
+  wait_for_predecessor();
+  const int c = blockIdx.x / kSoftWarpsV, w8 = blockIdx.x % kSoftWarpsV;
+  const Cut cut = reinterpret_cast<const Cut*>(a.partials)[c];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpk = a.Hq / a.Hkv;
+  const int row0 = cut.row0 + 32 * w8;
+  if (cut.count == 0 || row0 >= cut.rows) return;
+  const int row = min(row0 + lane, cut.rows - 1), qi = row / hpk;
+  T* dst = static_cast<T*>(a.out) + (cut.q0 + qi) * a.out_stride +
+           (long)(cut.kvh * hpk + row - qi * hpk) * D;
+  join_rows<T, D, D / 32>(
+      cut.count,
+      [&](int x) { return partial_of<D>(a, c + x, x == 0 ? 1 : 0) + w8 * VCfg<D>::kWarpState; },
+      lane, warp * (D / 32), row0 + lane < cut.rows, dst);
+}
+
+template <typename T, int D, bool PAGED>
+cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, bool skip_short,
+                     cudaStream_t stream) {
+  using C = VCfg<D>;
+  int unused = 0;
+  cudaError_t e = per_device_setup(a.device, &unused, [](int* v) {
+    *v = 1;
+    cudaFuncAttributes at{};
+    const cudaError_t e = cudaFuncGetAttributes(&at, varlen_attention_kernel<T, D, PAGED>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < kRegsV) return cudaErrorInvalidConfiguration;  // too few to redistribute
+    return cudaFuncSetAttribute(varlen_attention_kernel<T, D, PAGED>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::bytes(kMaxRequests));
+  });
+  if (e != cudaSuccess) return e;
+  CUtensorMap tk, tv;
+  if (PAGED) {
+    const long rows = ((long)a.num_pages * a.Hkv) << a.page_shift;
+    const int box = a.page_shift < 7 ? 1 << a.page_shift : kTileV;
+    if (!encode_bf16_map(&tk, a.k, rows, D, box) || !encode_bf16_map(&tv, a.v, rows, D, box))
+      return cudaErrorInvalidValue;
+  } else if (!encode_bf16_map(&tk, a.k, a.T, a.Hkv * D, kTileV, a.k_stride) ||
+             !encode_bf16_map(&tv, a.v, a.T, a.Hkv * D, kTileV, a.v_stride)) {
+    return cudaErrorInvalidValue;
+  }
+  const int grid = a.num_sms < kMaxGrid ? a.num_sms : kMaxGrid;
+  const bool join_here = (long)a.T * a.Hq >= 4L * 2 * kHalf * grid;
+  e = launch_pdl(varlen_attention_kernel<T, D, PAGED>, dim3(grid), dim3(kThreadsV), C::bytes(a.B),
+                 stream, tk, tv, a, scale_log2, skip_short, join_here);
+  if (e != cudaSuccess || join_here) return e;
+  return launch_pdl(varlen_join_kernel<T, D>, dim3(grid * kSoftWarpsV), dim3(256), 0, stream, a);
 }
 
 template <typename T>
-cudaError_t launch_simple(const VarlenAttnArgs& a, bool skip_short, cudaStream_t stream) {
-  const long warps = (long)a.T * a.Hq, blocks = (warps + 3) / 4;
-  if (a.D == 128)
-    varlen_attention_simple_kernel<T, 128><<<(unsigned)blocks, 128, 0, stream>>>(a, skip_short);
-  else
-    varlen_attention_simple_kernel<T, 64><<<(unsigned)blocks, 128, 0, stream>>>(a, skip_short);
-  return cudaGetLastError();
+cudaError_t launch_form(const VarlenAttnArgs& a, float scale_log2, bool skip_short,
+                        cudaStream_t stream) {
+  if (a.table == nullptr)
+    return a.D == 128 ? launch_t<T, 128, false>(a, scale_log2, skip_short, stream)
+                      : launch_t<T, 64, false>(a, scale_log2, skip_short, stream);
+  return a.D == 128 ? launch_t<T, 128, true>(a, scale_log2, skip_short, stream)
+                    : launch_t<T, 64, true>(a, scale_log2, skip_short, stream);
 }
 
 }  // namespace
 
-long varlen_partial_bytes(int D) { return paged_decode_partial_bytes(D); }
+long varlen_partial_bytes(int D) {
+  const long here = kMaxGrid * (long)sizeof(Cut) +
+                    kMaxGrid * 2L * (D == 128 ? VCfg<128>::kState : VCfg<64>::kState) * 4;
+  const long decode = paged_decode_partial_bytes(D);
+  return here > decode ? here : decode;
+}
 
 cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream) {
-  const float scale = a.sm_scale > 0.f ? a.sm_scale : 1.f / std::sqrt((float)a.D);
+  const float scale = (a.sm_scale > 0.f ? a.sm_scale : 1.f / std::sqrt((float)a.D)) * kLog2eV;
   const bool decode = a.table != nullptr && is_short(1, a.Hq / a.Hkv);
   if (decode) {
-    const cudaError_t e = launch_paged_decode(a, scale * kLog2eV, stream);
+    const cudaError_t e = launch_paged_decode(a, scale, stream);
     if (e != cudaSuccess || is_short(a.max_new, a.Hq / a.Hkv)) return e;
   }
-  return a.dtype == 0 ? launch_simple<__nv_bfloat16>(a, decode, stream)
-                      : launch_simple<__half>(a, decode, stream);
+  return a.dtype == 0 ? launch_form<__nv_bfloat16>(a, scale, decode, stream)
+                      : launch_form<__half>(a, scale, decode, stream);
 }
 
 }  // namespace kivi
