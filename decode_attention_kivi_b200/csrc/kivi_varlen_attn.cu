@@ -14,32 +14,36 @@
 // so long chunks are bound by the tensor cores and, equally, by the 128 * 256
 // exponentials of a tile (16 per SM and cycle: 2048 cycles, as long as its
 // products take).
-// The tiles of all items, in order, are cut into one contiguous range per CTA,
-// equal to within a tile whatever the lengths are; every CTA forms the prefix
-// sums that this needs from the device arrays.
+// The tiles of all items, in order, each item kItemCost tiles longer than it is,
+// are cut into one contiguous range per CTA, equal to within a tile whatever the
+// lengths are; every CTA forms the prefix sums that this needs from the device
+// arrays.
 //
 // Twelve warps (two idle), one CTA per SM:
-//   warp 9 (producer)  2D tensor copies of K and V tiles into a ring of four
+//   warp 8 (producer)  2D tensor copies of K and V tiles into a ring of four
 //                      slots, page by page (a box of min(page, 128) rows x 64
 //                      channels per lane) or in one piece;
-//   warp 8 (MMA)       one lane issues S_i = Q_i K^T (M = N = 128) for half i
-//                      into its score columns and O_i += P_i V, P_i read from
-//                      TMEM, where it lies over the first half of S_i; the two
-//                      halves alternate, so that the tensor cores work on one
-//                      while the other is in its softmax.  Only the 16-key steps
-//                      with keys that the half sees are issued;
+//   warps 9, 10 (MMA)  one elected lane each, for half i = 0, 1: S_i = Q_i K^T in
+//                      units of 64 keys (M = 128, N = 64) into one of the half's
+//                      two score buffers and O_i += P_i V, P_i read from TMEM,
+//                      where it lies over the first half of S_i.  The scores of
+//                      unit n + 2 follow the product of unit n, so that the
+//                      softmax of a half has a unit in hand while the tensor
+//                      cores work on the other.  Units and 16-key steps without
+//                      a key that the half sees are left out;
 //   warps 0-7          one row per thread (its TMEM lane): the row of S from
-//                      TMEM, the mask where the tile needs one, the online
+//                      TMEM, the mask where the unit needs one, the online
 //                      softmax in base 2, P back to TMEM.  O is rescaled only
-//                      when a row's maximum grew by more than 2^8 (up to then
-//                      the stale maximum is kept: weights stay below 2^8 and
-//                      O / l is unchanged).  The next item's Q rows are fetched
-//                      during the last tile of this one.
+//                      when a row's maximum grew by more than kSlack (up to then
+//                      the stale maximum is kept; O / l is unchanged).  The next
+//                      item's Q rows are fetched during the last unit of this
+//                      one.
 // An item that lies in several CTAs leaves a partial (m, l, O in fp32) per CTA,
 // joined in CTA order, so results do not depend on the order of arrival: by the
 // warp that arrives last (a ticket per CTA and warp), or, where few items are
 // cut into many pieces, by a second kernel over all SMs.
-// TMEM: S_0 and S_1 at columns 0 and 128, O_0 at 256, O_1 behind it.
+// TMEM: two buffers of S_0 at columns 0 and 64, of S_1 at 128 and 192, O_0 at 256,
+// O_1 behind it.
 // Every wait is bounded; a wait that runs out sets the status word, and what was
 // issued is drained before TMEM is released.
 #include <cmath>
@@ -54,17 +58,28 @@ namespace {
 constexpr float kLog2eV = 1.4426950408889634f;
 constexpr int kHalf = 128;             // rows of a half = TMEM lanes
 constexpr int kTileV = 128;            // keys per tile
+constexpr int kUnit = 64;              // keys of a score buffer
 constexpr int kSoftWarpsV = 8;
-constexpr int kMmaWarpV = kSoftWarpsV, kProducerWarpV = kSoftWarpsV + 1;
-constexpr int kThreadsV = (kSoftWarpsV + 4) * 32;  // three warpgroups; two warps of the last idle
+constexpr int kProducerWarpV = kSoftWarpsV, kMmaWarpV = kSoftWarpsV + 1;  // and + 2: by half
+constexpr int kThreadsV = (kSoftWarpsV + 4) * 32;  // three warpgroups; one warp of the last idle
 // Registers per thread at launch, and after the softmax warpgroups took what the third gave up.
 constexpr int kRegsV = 168, kRegsSoft = 208, kRegsRest = 88;
 static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegsV, "a larger sum would wait forever");
 constexpr int kSlabV = 128 * 128;      // 128 rows of 64 channels
 constexpr int kSlots = 4;              // K and V tiles in flight
 constexpr uint32_t kTmemColsV = 512;
-constexpr float kSlackV = 8.f;         // log2 growth of a row maximum before O is rescaled
 constexpr int kMinTilesV = 4;          // tiles per CTA at least
+constexpr int kItemCost = 1;           // tiles that an item's start and end are worth
+constexpr int kChunk = 32;             // scores turned into weights at a time
+#ifndef POLY
+#define POLY 2
+#endif
+constexpr int kPolyOf8 = POLY;            // pairs of eight whose exponentials the fp32 pipe takes
+// log2 growth of a row maximum before O is rescaled: the weights stay below 2^kSlack, far inside
+// what the type and the 32-bit sums hold, and a larger slack costs no accuracy (the roundings are
+// relative); fp16 weights must stay below 2^16.
+template <typename T>
+constexpr float kSlack = Elem<T>::kBf16 ? 32.f : 14.f;
 // one item cut into pieces: what the joining kernel needs
 struct Cut {
   int count, q0, kvh, row0, rows, pad[3];
@@ -89,15 +104,19 @@ struct VCfg {
   static_assert(kColO + 2 * D <= kTmemColsV, "TMEM plan");
 };
 
-// Tiles that the half of rows row0 .. row0 + 127 of an item sees; at least one where it has rows.
-__device__ __forceinline__ int half_tiles(const Request& r, int rows, int row0, int hpk) {
+// Units that the half of rows row0 .. row0 + 127 of an item sees; at least one where it has rows.
+__device__ __forceinline__ int half_units(const Request& r, int rows, int row0, int hpk) {
   if (row0 >= rows) return 0;
   const int kmax = min(last_key(r, (min(row0 + kHalf, rows) - 1) / hpk), r.L - 1);
-  return kmax < 0 ? 1 : kmax / kTileV + 1;
+  return kmax < 0 ? 1 : kmax / kUnit + 1;
 }
+constexpr int kUnits = kTileV / kUnit;
+__device__ __forceinline__ int tiles_of_units(int n) { return (n + kUnits - 1) / kUnits; }
+// Tiles of an item: those of its last rows, which see the most keys.
 __device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, int hpk) {
-  return max(half_tiles(r, rows, tt * 2 * kHalf, hpk),
-             half_tiles(r, rows, tt * 2 * kHalf + kHalf, hpk));
+  if (tt * 2 * kHalf >= rows) return 0;
+  const int kmax = min(last_key(r, (min((tt + 1) * 2 * kHalf, rows) - 1) / hpk), r.L - 1);
+  return kmax < 0 ? 1 : kmax / kTileV + 1;
 }
 
 struct Ranges {
@@ -109,12 +128,78 @@ struct Ranges {
   }
 };
 
-// A CTA's piece of an item: tiles j0 .. j1 - 1 of nt, half i active below e[i].
+// A CTA's piece of an item: tiles j0 .. j1 - 1 of nt, for half i the units kUnits * j0 .. ei - 1.
 struct Piece {
-  int t;  // tiles before this one in the whole call
-  int b, kvh, tt, rows, j0, j1, nt, e[2];
+  int t0;  // where the item's tiles begin in the whole call, behind its cost
+  int b, kvh, tt, rows, j0, j1, nt, e0, e1;
   Request r;
+  __device__ __forceinline__ int end(int half) const { return half ? e1 : e0; }
 };
+
+// 2^x of two values: on the special function unit, or (kPoly) by 2^n (1 + f (c1 + f (c2 + ...))) with
+// n = round(x), f = x - n in [-1/2, 1/2] on the fp32 pipe, the exponent added to the bits.  The
+// coefficients minimise the largest relative error with value 1 at f = 0: 2^-13.3 at degree 3
+// (bf16 weights, half a step 2^-9), 2^-18.4 at degree 4 (fp16).  x below -127 gives 0.
+template <typename T>
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves round(x) in the low bits
+  x.x = fmaxf(x.x, -127.f);
+  x.y = fmaxf(x.y, -127.f);
+  const float2 r = add2(x, make_float2(kRound, kRound));
+  const float2 n = add2(r, make_float2(-kRound, -kRound));
+  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+  float2 y;
+  if (Elem<T>::kBf16) {
+    y = make_float2(0.05500906f, 0.05500906f);
+    y = fma2(y, f, make_float2(0.24221097f, 0.24221097f));
+    y = fma2(y, f, make_float2(0.6932829f, 0.6932829f));
+  } else {
+    y = make_float2(0.009582576f, 0.009582576f);
+    y = fma2(y, f, make_float2(0.05590683f, 0.05590683f));
+    y = fma2(y, f, make_float2(0.24024107f, 0.24024107f));
+    y = fma2(y, f, make_float2(0.6931241f, 0.6931241f));
+  }
+  y = fma2(y, f, make_float2(1.f, 1.f));
+  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23)),
+                     __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23)));
+}
+
+__device__ __forceinline__ float exp2_in_order(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void max_in_order(float& m, float a, float b) {
+  asm volatile("max.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(a), "f"(b));
+}
+
+// Weights 2^(scale s - mu) of kChunk scores as packed pairs, and their sum.  With kMax the maxima
+// mx4 of all kUnit scores are formed between the exponentials, whose unit takes one warp
+// instruction in eight cycles: the order is kept by volatile statements.
+template <typename T, bool kMax = false>
+__device__ __forceinline__ void weights(const float* s, float scale, float mu,
+                                        uint32_t (&pk)[kChunk / 2], float2& sum, float (&mx4)[4]) {
+  const float2 sc = make_float2(scale, scale), nm = make_float2(-mu, -mu);
+  float2 t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < kChunk / 2; ++c) {
+    float2 x = fma2(make_float2(s[2 * c], s[2 * c + 1]), sc, nm);
+    if (kMax) {
+      x.x = exp2_in_order(x.x);
+      max_in_order(mx4[2 * (c & 1)], s[4 * c], s[4 * c + 2]);
+      x.y = exp2_in_order(x.y);
+      max_in_order(mx4[2 * (c & 1) + 1], s[4 * c + 1], s[4 * c + 3]);
+    } else if ((c & 7) >= 8 - kPolyOf8) {
+      x = exp2_poly<T>(x);
+    } else {
+      x.x = fast_exp2(x.x);
+      x.y = fast_exp2(x.y);
+    }
+    t[c & 1] = add2(t[c & 1], x);
+    pk[c] = Elem<T>::pack(x.x, x.y);
+  }
+  sum = add2(t[0], t[1]);
+}
 
 // The rows' joined output from `count` partials, in order; src(w) is a warp's state.
 template <typename T, int D, int C4, typename Src>
@@ -168,13 +253,13 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);  // [kSlots]
   uint64_t* empty = full + kSlots;
   uint64_t* q_full = empty + kSlots;  // [2] each, by half
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
-  uint64_t* drained = o_done + 2;
+  uint64_t* s_full = q_full + 2;      // [4], by half and buffer
+  uint64_t* p_full = s_full + 4;      // [4]
+  uint64_t* o_done = p_full + 4;      // [4], the product of the buffer's weights
+  uint64_t* drained = o_done + 4;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, kvh, tt, j of the CTA's first tile
+  int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, kvh, tt, t0 of the CTA's first item
   int* s_sum = s_start + 4;                           // [kThreadsV / 32]
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,15 +269,17 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     *s_abort = 0;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], kHalf);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kHalf);
-      mbar_init(&o_done[i], 1);
     }
-    mbar_init(drained, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&p_full[i], kHalf);
+    }
+    mbar_init(drained, 2);
     fence_mbar_init();
   }
   if (warp == kMmaWarpV) {
@@ -216,14 +303,14 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     const int rows = r.n * hpk, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
     long long v = 0;
     if (items <= 4)
-      for (int tt = 0; tt < items; ++tt) v += item_tiles(r, rows, tt, hpk);
+      for (int tt = 0; tt < items; ++tt) v += kItemCost + item_tiles(r, rows, tt, hpk);
     // requests of many items: the warp's lanes share them
     for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
       const int from = __ffs(left) - 1;
       const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
       const int rrows = rr.n * hpk;
       long long sum = 0;
-      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_tiles(rr, rrows, tt, hpk);
+      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += kItemCost + item_tiles(rr, rrows, tt, hpk);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == from) v = sum;
@@ -284,7 +371,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     const int kvh = (t_begin - prefix[lo]) / per_head;
     int x = t_begin - prefix[lo] - kvh * per_head;  // tiles to pass within the head
     for (int t0 = 0;; t0 += 32) {
-      const int v = item_tiles(r, rows, t0 + lane, hpk);
+      const int v = kItemCost + item_tiles(r, rows, t0 + lane, hpk);
       int inc = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -297,7 +384,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
           s_start[0] = lo;
           s_start[1] = kvh;
           s_start[2] = t0 + lane;
-          s_start[3] = x - (inc - v);
+          s_start[3] = t_begin - (x - (inc - v)) + kItemCost;
         }
         break;
       }
@@ -306,15 +393,13 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   }
   __syncthreads();
 
-  auto set_item = [&](Piece& p, int j0) {
+  auto set_item = [&](Piece& p) {
     const int row0 = p.tt * 2 * kHalf;
-    p.e[0] = half_tiles(p.r, p.rows, row0, hpk);
-    p.e[1] = half_tiles(p.r, p.rows, row0 + kHalf, hpk);
-    p.nt = max(p.e[0], p.e[1]);
-    p.j0 = j0;
-    p.j1 = min(p.nt, j0 + (t_end - p.t));
-    p.e[0] = min(p.e[0], p.j1);
-    p.e[1] = min(p.e[1], p.j1);
+    p.nt = item_tiles(p.r, p.rows, p.tt, hpk);
+    p.j0 = max(0, t_begin - p.t0);
+    p.j1 = min(p.nt, t_end - p.t0);
+    p.e0 = min(half_units(p.r, p.rows, row0, hpk), kUnits * p.j1);
+    p.e1 = min(half_units(p.r, p.rows, row0 + kHalf, hpk), kUnits * p.j1);
   };
   auto set_request = [&](Piece& p, int b) {
     bool bad;
@@ -324,19 +409,20 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   };
   auto first_piece = [&]() {
     Piece p;
-    p.t = t_begin;
+    p.t0 = t_end;
     if (t_begin < t_end) {
       set_request(p, s_start[0]);
       p.kvh = s_start[1];
       p.tt = s_start[2];
-      set_item(p, s_start[3]);
+      p.t0 = s_start[3];
+      set_item(p);
     }
     return p;
   };
-  // the piece after p; it is there if its t < t_end
+  // the piece after p; it is there if its t0 < t_end
   auto next_piece = [&](Piece& p) {
-    p.t += p.j1 - p.j0;
-    if (p.t >= t_end) return;
+    p.t0 += p.nt + kItemCost;
+    if (p.t0 >= t_end) return;
     if (++p.tt * 2 * kHalf >= p.rows) {
       p.tt = 0;
       if (++p.kvh == a.Hkv) {
@@ -346,15 +432,14 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
         set_request(p, b);
       }
     }
-    set_item(p, 0);
+    set_item(p);
   };
   auto fail = [&]() {
     *s_abort = 1;
     atomicOr(a.status, kPagedTimeout);
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-    const bool w = mbar_wait_bounded(bar, parity);
-    return __all_sync(0xffffffffu, w && *s_abort == 0);
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, s_abort));
   };
 
   if (warp < kSoftWarpsV) {
@@ -389,84 +474,98 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       fence_proxy_async();  // Q is read by the tensor cores
       mbar_arrive(&q_full[hf]);
     };
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0;  // phases by buffer: bit b is that of its next scores, its last product had the other
+    int u = 0;  // tiles of the pieces before, as the producer counts them
     bool ok = true;
     Cut cut{0, 0, 0, 0, 0, {0, 0, 0}};
     Piece p = first_piece();
-    if (p.t < t_end && p.e[hf] > p.j0) {
+    if (p.t0 < t_end && p.end(hf) > kUnits * p.j0) {
       fetch_q(p);
       q_here();
     }
-    while (ok && p.t < t_end) {
+    while (ok && p.t0 < t_end) {
       Piece nx = p;
       next_piece(nx);
-      const bool more = nx.t < t_end && nx.e[hf] > nx.j0;
-      const bool active = p.e[hf] > p.j0;
+      const int n0 = kUnits * p.j0, e = p.end(hf);
+      const bool more = nx.t0 < t_end && nx.end(hf) > kUnits * nx.j0;
+      const bool active = e > n0;
       const int row = p.tt * 2 * kHalf + hf * kHalf + r, qi = row / hpk;
       const bool real = row < p.rows;
       const int last = real ? min(last_key(p.r, qi), p.r.L - 1) : -1;
-      // tiles that end behind this key need the mask
+      // units that end behind this key need the mask
       const int clear = min(last_key(p.r, (row - r) / hpk), p.r.L - 1);
       float m = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
-      for (int j = p.j0; j < p.e[hf]; ++j) {
-        if (!(ok = wait_warp(&s_full[hf], ns++ & 1u))) break;
+      for (int n = n0; n < e; ++n) {
+        const int buf = n % kUnits;
+        const uint32_t col = col_s + buf * kUnit;
+        if (!(ok = wait_warp(&s_full[2 * hf + buf], ns >> buf & 1u))) break;
+        ns ^= 1u << buf;
         tc::fence_after();
-        if (more && j + 1 == p.e[hf]) fetch_q(nx);  // this item's scores are done with Q
-        float s[kTileV];
-        tc::ld_x128(col_s, s);
-        const int key0 = j * kTileV;
-        if (key0 + kTileV - 1 > clear) {
+        if (more && n + 1 == e) fetch_q(nx);  // this item's scores are done with Q
+        float s[kUnit];
+        tc::ld_x64(col, s);
+        const int nv = p.r.L - n / kUnits * kTileV;  // keys of the tile
+        if (buf == 0 && nv > 0 && nv < kTileV && (nv & 15)) {
+          // V rows behind the last key up to a whole step: a weight of 0 times NaN (both halves
+          // write the zeros)
+          const int x = u + 2 * (n / kUnits - p.j0) + 1;
+          if (!(ok = wait_warp(&full[x % kSlots], (uint32_t)(x / kSlots) & 1u))) break;
+          unsigned char* vs = smem + C::kOffRing + (x % kSlots) * C::kTileBytes;
+          for (int y = r; y < (16 - (nv & 15)) * C::kSlabs * 8; y += kHalf) {
+            const int row_v = nv + y / (C::kSlabs * 8), rest = y % (C::kSlabs * 8);
+            *reinterpret_cast<uint4*>(vs + (rest / 8) * kSlabV + row_v * 128 + 16 * (rest % 8)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+        }
+        const int key0 = n * kUnit;
+        if (key0 + kUnit - 1 > clear) {
           const int lim = last - key0;
 #pragma unroll
-          for (int c = 0; c < kTileV; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+          for (int c = 0; c < kUnit; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
         }
-        float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < kTileV; c += 8)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mx4[x] = c + 4 + x < kTileV ? fmax3(mx4[x], s[c + x], s[c + 4 + x]) : fmaxf(mx4[x], s[c + x]);
+        // the weights with the maximum so far, while the unit's is formed; they are formed again
+        // in the few units where it grew
+        float mu = m == -INFINITY ? 0.f : m;
+        float2 sum, sum1;
+        uint32_t pk[kChunk / 2], pk1[kChunk / 2];
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        weights<T, true>(s, scale_log2, mu, pk, sum, mx4);
         const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale_log2;
-        const bool grow = mx > m + kSlackV;  // always where m = -inf and a key is seen
-        const float mn = grow ? mx : m, mu = mn == -INFINITY ? 0.f : mn;
-        const float al = fast_exp2(m - mu);  // 1 where kept, 0 at a row's first keys
-        m = mn;
-        // S(j) came after P V of tile j - 1 on the tensor cores: O is complete up to it
-        if (j > p.j0 && __any_sync(0xffffffffu, grow)) {
+        const bool grow = mx > m + kSlack<T>;  // always where m = -inf and a key is seen
+        if (__any_sync(0xffffffffu, grow)) {
+          const float al = grow ? fast_exp2(m - mx) : 1.f;  // 0 at a row's first keys
+          if (grow) m = mu = mx;
+          l *= al;
+          weights<T>(s, scale_log2, mu, pk, sum, mx4);
+          if (n > n0) {  // P V up to the unit before must be in O
+            if (!(ok = wait_warp(&o_done[2 * hf + (buf ^ 1)], ~ns >> (buf ^ 1) & 1u))) break;
+            tc::fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tc::ld_x32(col_o + c0, o);
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              float o[32];
+              tc::ld_x32(col_o + c0, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= grow ? al : 1.f;
-            tc::st_x32(col_o + c0, o);
+              for (int i = 0; i < 32; ++i) o[i] *= al;
+              tc::st_x32(col_o + c0, o);
+            }
           }
         }
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-mu, -mu);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float2 x = fma2(make_float2(s[64 * q + 2 * c], s[64 * q + 2 * c + 1]), sc, nm);
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            sum[c & 1] = add2(sum[c & 1], x);
-            pk[c] = Elem<T>::pack(x.x, x.y);
-          }
-          tc::st_x32(col_s + 32 * q, pk);
-        }
-        l = l * (grow ? al : 1.f) + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+        tc::st_x16(col, pk);
+        weights<T>(s + kChunk, scale_log2, mu, pk1, sum1, mx4);
+        tc::st_x16(col + kChunk / 2, pk1);
+        sum = add2(sum, sum1);
+        l += sum.x + sum.y;
         tc::wait_st();
         tc::fence_before();
-        mbar_arrive(&p_full[hf]);
+        mbar_arrive(&p_full[2 * hf + buf]);
       }
       if (!ok) break;
       if (!active && more) fetch_q(nx);
       if (more) q_here();
       if (active) {
-        if (!(ok = wait_warp(&o_done[hf], no++ & 1u))) break;
+        const int buf = (e - 1) % kUnits;
+        if (!(ok = wait_warp(&o_done[2 * hf + buf], ~ns >> buf & 1u))) break;
         tc::fence_after();
       }
       T* dst = static_cast<T*>(a.out) + (p.r.q0 + (real ? qi : 0)) * a.out_stride +
@@ -505,7 +604,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
         }
         part[32 * D + lane] = m;
         part[32 * (D + 1) + lane] = l;
-        const int first = p.t - p.j0, c0 = sp.cta_of(first), c1 = sp.cta_of(first + p.nt - 1);
+        const int c0 = sp.cta_of(p.t0), c1 = sp.cta_of(p.t0 + p.nt - 1);
         if (join_here) {
           __threadfence();
           __syncwarp();
@@ -524,6 +623,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
           cut = Cut{c1 - c0 + 1, p.r.q0, p.kvh, p.tt * 2 * kHalf, p.rows, {0, 0, 0}};
         }
       }
+      u += 2 * (p.j1 - p.j0);
       p = nx;
     }
     if (!ok) fail();
@@ -538,7 +638,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       const int outside = PAGED ? (a.num_pages * a.Hkv) << a.page_shift : 0;  // rows of zeros
       int u = 0;
       bool ok = true;
-      for (Piece p = first_piece(); ok && p.t < t_end; next_piece(p)) {
+      for (Piece p = first_piece(); ok && p.t0 < t_end; next_piece(p)) {
         for (int j = p.j0; ok && j < p.j1; ++j) {
           const int key = j * kTileV + part * box;
           const bool mine = lane < boxes && key < p.r.L;
@@ -574,90 +674,83 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       // every copy issued lands before the CTA may exit
       for (int i = max(u - kSlots, 0); i < u; ++i)
         if (!mbar_wait_bounded(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u)) fail();
-    } else if (warp == kMmaWarpV) {
-      // ---- MMA ----
-      constexpr bool kBf16 = sizeof(T) == 2 && Elem<T>::kBf16;
-      constexpr uint32_t id_s = tc::idesc_16bit(kHalf, kTileV, false, kBf16);
-      constexpr uint32_t id_o = tc::idesc_16bit(kHalf, D, true, kBf16);
-      const uint32_t q_base = smem_addr(smem), ring = smem_addr(smem + C::kOffRing);
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-      int u = 0;  // tiles consumed, as the producer counts them
+    } else if (warp != kMmaWarpV && warp != kMmaWarpV + 1) {
+      // idle
+    } else if (tc::elect_one()) {
+      // ---- MMA of half i, by one lane ----
+      const int i = warp - kMmaWarpV;
+      constexpr uint32_t id_s = tc::idesc_16bit(kHalf, kUnit, false, Elem<T>::kBf16);
+      constexpr uint32_t id_o = tc::idesc_16bit(kHalf, D, true, Elem<T>::kBf16);
+      constexpr int kTile16 = C::kTileBytes / 16, kUnit16 = kUnit * 128 / 16;
+      // descriptors of the half's Q and of ring slot 0; their low words count 16 bytes
+      const uint64_t qd = tc::desc_sw128(smem_addr(smem), 16, 1024) + i * kTile16;
+      const uint64_t kd = tc::desc_sw128(smem_addr(smem + C::kOffRing), 16, 1024);
+      const uint64_t vd = tc::desc_sw128(smem_addr(smem + C::kOffRing), kSlabV, 1024);
+      const uint32_t ts = tmem + i * kTileV, to = tmem + C::kColO + i * D;
+      uint32_t nq = 0, np = 0;  // phases; bit b of np: of buffer b
+      int u = 0;  // tiles of the pieces before, as the producer counts them
       bool ok = true;
-      auto wait_tile = [&](int i) { return wait_warp(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u); };
-      auto scores = [&](int i, int tile) {
-        if (lane == 0) {
-  #pragma unroll
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, s_abort); };
+      auto wait_tile = [&](int x) { return wait(&full[x % kSlots], (uint32_t)(x / kSlots) & 1u); };
+      for (Piece p = first_piece(); ok && p.t0 < t_end; next_piece(p)) {
+        const int n0 = kUnits * p.j0, e = p.end(i);
+        // keys that some row of the half sees
+        const int seen =
+            min(last_key(p.r, (min(p.tt * 2 * kHalf + (i + 1) * kHalf, p.rows) - 1) / hpk) + 1, p.r.L);
+        // the scores of unit n from K tile x, released behind the last unit in it
+        auto scores = [&](int n, int x) {
+          const uint64_t kt = kd + (x % kSlots) * kTile16 + (n % kUnits) * kUnit16;
+#pragma unroll
           for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = (s >> 2) * kSlabV + (s & 3) * 32;
-            tc::mma_bf16(tmem + i * kTileV, tc::desc_sw128(q_base + i * C::kTileBytes + off, 16, 1024),
-                         tc::desc_sw128(ring + (tile % kSlots) * C::kTileBytes + off, 16, 1024), id_s,
-                         s > 0);
+            const int off = ((s >> 2) * kSlabV + (s & 3) * 32) / 16;
+            tc::mma_bf16(ts + (n % kUnits) * kUnit, qd + off, kt + off, id_s, s > 0);
           }
-          tc::commit(&s_full[i]);
-        }
-      };
-      for (Piece p = first_piece(); ok && p.t < t_end; next_piece(p)) {
-        const int row0 = p.tt * 2 * kHalf;
-        int seen[2];  // keys that some row of the half sees
-        for (int i = 0; i < 2; ++i)
-          seen[i] = min(last_key(p.r, (min(row0 + (i + 1) * kHalf, p.rows) - 1) / hpk) + 1, p.r.L);
-        ok = wait_tile(u);
-        for (int i = 0; ok && i < 2; ++i) {
-          if (p.e[i] <= p.j0) continue;
-          ok = wait_warp(&q_full[i], nq[i]++ & 1u);
-          if (!ok) break;
+          tc::commit(&s_full[2 * i + n % kUnits]);
+          if ((n + 1) % kUnits == 0 || n + 1 == e) tc::commit(&empty[x % kSlots]);
+        };
+        if (e > n0) {
+          if (!(ok = wait(q_full + i, nq++ & 1u) && wait_tile(u))) break;
           tc::fence_after();
-          scores(i, u);
+          scores(n0, u);
+          if (n0 + 1 < e) scores(n0 + 1, u);
         }
-        if (ok && lane == 0) tc::commit(&empty[u % kSlots]);
-        for (int j = p.j0; ok && j < p.j1; ++j) {
-          const int tile_v = u + 1, tile_k = u + 2;
-          u += 2;
-          if (!(ok = wait_tile(tile_v))) break;
-          const uint32_t vb = ring + (tile_v % kSlots) * C::kTileBytes;
-          const int nv = min(kTileV, p.r.L - j * kTileV);
-          if (nv > 0 && (nv & 15)) {  // rows behind the last key: a weight of 0 times NaN
-            unsigned char* vs = smem + C::kOffRing + (tile_v % kSlots) * C::kTileBytes;
-            for (int x = lane; x < (16 - (nv & 15)) * C::kSlabs * 8; x += 32) {
-              const int row = nv + x / (C::kSlabs * 8), rest = x % (C::kSlabs * 8);
-              *reinterpret_cast<uint4*>(vs + (rest / 8) * kSlabV + row * 128 + 16 * (rest % 8)) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async();
-            __syncwarp();
+        int x = u + 1;  // the V tile of unit n; K of the next tile is x + 1
+        for (int n = n0; n < e; ++n) {
+          const int half = n % kUnits;
+          if (half == 0 && !(ok = wait_tile(x) && (n + 2 >= e || wait_tile(x + 1)))) break;
+          const int steps = (min(kUnit, seen - n * kUnit) + 15) >> 4;
+          const uint64_t vt = vd + (x % kSlots) * kTile16 + half * kUnit16;
+          const uint32_t tp = ts + half * kUnit;
+          if (!(ok = wait(p_full + 2 * i + half, np >> half & 1u))) break;
+          np ^= 1u << half;
+          tc::fence_after();
+          if (steps == kUnit / 16) {
+#pragma unroll
+            for (int s = 0; s < kUnit / 16; ++s)
+              tc::mma_16bit_tmem_a(to, tp + s * 8, vt + s * 128, id_o, n > n0 || s > 0);
+          } else {
+            for (int s = 0; s < steps; ++s)
+              tc::mma_16bit_tmem_a(to, tp + s * 8, vt + s * 128, id_o, n > n0 || s > 0);
           }
-          const int e_max = max(p.e[0], p.e[1]);
-          for (int i = 0; i < 2; ++i) {
-            if (j < p.e[i]) {
-              if (!(ok = wait_warp(&p_full[i], np[i]++ & 1u))) break;
-              tc::fence_after();
-              if (lane == 0) {
-                const int steps = (min(kTileV, seen[i] - j * kTileV) + 15) >> 4;
-                for (int s = 0; s < steps; ++s)
-                  tc::mma_16bit_tmem_a(tmem + C::kColO + i * D, tmem + i * kTileV + s * 8,
-                                       tc::desc_sw128(vb + s * 16 * 128, kSlabV, 1024), id_o,
-                                       j > p.j0 || s > 0);
-                if (j + 1 == p.e[i]) tc::commit(&o_done[i]);
-              }
-            }
-            if (i == 1 && lane == 0) tc::commit(&empty[tile_v % kSlots]);
-            if (j + 1 < p.e[i]) {
-              if (!(ok = wait_tile(tile_k))) break;
-              tc::fence_after();
-              scores(i, tile_k);
-            }
-          }
-          if (ok && j + 1 < e_max && lane == 0) tc::commit(&empty[tile_k % kSlots]);
+          tc::commit(o_done + 2 * i + half);
+          if (n + 2 < e) scores(n + 2, x + 1);
+          if (half == kUnits - 1 || n + 1 == e) tc::commit(&empty[x % kSlots]);
+          x += 2 * half;
         }
+        // tiles that only the other half sees
+        for (int j = max(p.j0, tiles_of_units(e)); ok && j < p.j1; ++j)
+          for (int y = u + 2 * (j - p.j0), z = y + 2; ok && y < z; ++y) {
+            ok = wait_tile(y);
+            if (ok) tc::commit(&empty[y % kSlots]);
+          }
+        u += 2 * (p.j1 - p.j0);
       }
       if (!ok) fail();
       // all that was issued has completed before TMEM is released
-      if (lane == 0) {
-        tc::commit(drained);
-        if (!mbar_wait_bounded(drained, 0)) fail();
-      }
-      __syncwarp();
+      tc::commit(drained);
+      if (!mbar_wait_bounded(drained, 0)) fail();
     }
+    __syncwarp();
   }
   allow_successor();
   tc::fence_before();
