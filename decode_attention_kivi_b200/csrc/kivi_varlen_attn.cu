@@ -71,10 +71,6 @@ constexpr uint32_t kTmemColsV = 512;
 constexpr int kMinTilesV = 4;          // tiles per CTA at least
 constexpr int kItemCost = 1;           // tiles that an item's start and end are worth
 constexpr int kChunk = 32;             // scores turned into weights at a time
-#ifndef POLY
-#define POLY 2
-#endif
-constexpr int kPolyOf8 = POLY;            // pairs of eight whose exponentials the fp32 pipe takes
 // log2 growth of a row maximum before O is rescaled: the weights stay below 2^kSlack, far inside
 // what the type and the 32-bit sums hold, and a larger slack costs no accuracy (the roundings are
 // relative); fp16 weights must stay below 2^16.
@@ -136,34 +132,6 @@ struct Piece {
   __device__ __forceinline__ int end(int half) const { return half ? e1 : e0; }
 };
 
-// 2^x of two values: on the special function unit, or (kPoly) by 2^n (1 + f (c1 + f (c2 + ...))) with
-// n = round(x), f = x - n in [-1/2, 1/2] on the fp32 pipe, the exponent added to the bits.  The
-// coefficients minimise the largest relative error with value 1 at f = 0: 2^-13.3 at degree 3
-// (bf16 weights, half a step 2^-9), 2^-18.4 at degree 4 (fp16).  x below -127 gives 0.
-template <typename T>
-__device__ __forceinline__ float2 exp2_poly(float2 x) {
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves round(x) in the low bits
-  x.x = fmaxf(x.x, -127.f);
-  x.y = fmaxf(x.y, -127.f);
-  const float2 r = add2(x, make_float2(kRound, kRound));
-  const float2 n = add2(r, make_float2(-kRound, -kRound));
-  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
-  float2 y;
-  if (Elem<T>::kBf16) {
-    y = make_float2(0.05500906f, 0.05500906f);
-    y = fma2(y, f, make_float2(0.24221097f, 0.24221097f));
-    y = fma2(y, f, make_float2(0.6932829f, 0.6932829f));
-  } else {
-    y = make_float2(0.009582576f, 0.009582576f);
-    y = fma2(y, f, make_float2(0.05590683f, 0.05590683f));
-    y = fma2(y, f, make_float2(0.24024107f, 0.24024107f));
-    y = fma2(y, f, make_float2(0.6931241f, 0.6931241f));
-  }
-  y = fma2(y, f, make_float2(1.f, 1.f));
-  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23)),
-                     __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23)));
-}
-
 __device__ __forceinline__ float exp2_in_order(float x) {
   float y;
   asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -189,8 +157,6 @@ __device__ __forceinline__ void weights(const float* s, float scale, float mu,
       max_in_order(mx4[2 * (c & 1)], s[4 * c], s[4 * c + 2]);
       x.y = exp2_in_order(x.y);
       max_in_order(mx4[2 * (c & 1) + 1], s[4 * c + 1], s[4 * c + 3]);
-    } else if ((c & 7) >= 8 - kPolyOf8) {
-      x = exp2_poly<T>(x);
     } else {
       x.x = fast_exp2(x.x);
       x.y = fast_exp2(x.y);
