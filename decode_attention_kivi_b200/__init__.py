@@ -290,16 +290,23 @@ class Bf16Attention:
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # KIVI_BF16, KIVI_FP16
 
 
-def _one_device(first: torch.Tensor, *rest) -> None:
-    """All tensors on one CUDA device, the current one (whose stream the call takes)."""
-    dev = first.device
-    if dev.type != "cuda":
+def _one_device(*tensors) -> int:
+    """All tensors on one CUDA device, the current one (whose stream the call takes): its index."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device is needed")
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but cuda:{torch.cuda.current_device()} is current")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
+    return dev
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The raw stream of a call; the current one is asked for without a Stream object around it,
+    which takes as long as a launch."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -350,7 +357,8 @@ def kivi_attention_workspace_bytes(num_kv_heads: int, num_q_heads: int, head_dim
 def kivi_attention_status(workspace: torch.Tensor, stream=None) -> int:
     """Reads and clears the status word of an attention workspace (0: nothing reported)."""
     code = ctypes.c_uint32()
-    rc = lib().kivi_attention_status(_ptr(workspace, name="workspace"), _stream(stream),
+    dev = _one_device(workspace)
+    rc = lib().kivi_attention_status(_ptr(workspace, name="workspace"), _stream_on(dev, stream),
                                      ctypes.byref(code))
     if rc not in (0, 7):
         check(rc, "kivi_attention_status")
@@ -366,7 +374,7 @@ def kivi_paged_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_tab
     block_table [B][W] from the stack free_pages / num_free by what new_tokens [B] need beyond
     lengths [B], and fills kv_lengths [B], num_free_out [1], offsets [B+1], slots and positions
     [rows].  Negative new_tokens release a request.  All int32; `status` [1] collects failures."""
-    _one_device(lengths, new_tokens, block_table, free_pages, num_free, kv_lengths, num_free_out,
+    dev = _one_device(lengths, new_tokens, block_table, free_pages, num_free, kv_lengths, num_free_out,
                 offsets, slots, positions, status)
     if block_table.dim() != 2 or free_pages.dim() != 1 or slots.dim() != 1:
         raise ValueError("block_table [B][W], free_pages [num_pages], slots [rows]")
@@ -379,7 +387,7 @@ def kivi_paged_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_tab
         pages, page_size, _int_array(kv_lengths, (B,), "kv_lengths"),
         _int_array(num_free_out, (1,), "num_free_out"), _int_array(offsets, (B + 1,), "offsets"),
         _int_array(slots, (rows,), "slots"), _int_array(positions, (rows,), "positions"), rows,
-        _int_array(status, (1,), "status"), _stream(stream)), "kivi_paged_assign")
+        _int_array(status, (1,), "status"), _stream_on(dev, stream)), "kivi_paged_assign")
 
 
 def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
@@ -387,7 +395,7 @@ def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Ten
                       status: torch.Tensor | None = None, stream=None) -> None:
     """Writes k_new, v_new [rows][Hkv][D] into the slots [rows] of one layer's pages
     [num_pages][Hkv][page_size][D] (bf16 or fp16); rows with a negative slot are skipped."""
-    _one_device(k_new, v_new, slots, k_pages, v_pages, status)
+    dev = _one_device(k_new, v_new, slots, k_pages, v_pages, status)
     pages, hkv, page, dim = _pages(k_pages, v_pages, k_new.dtype)
     rows = k_new.shape[0]
     if k_new.shape != (rows, hkv, dim) or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
@@ -396,7 +404,7 @@ def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Ten
         k_new.data_ptr(), _row_stride(k_new, "k_new"), v_new.data_ptr(),
         _row_stride(v_new, "v_new"), _int_array(slots, (rows,), "slots"), rows,
         k_pages.data_ptr(), v_pages.data_ptr(), pages, page, hkv, dim,
-        None if status is None else _int_array(status, (1,), "status"), _stream(stream)),
+        None if status is None else _int_array(status, (1,), "status"), _stream_on(dev, stream)),
         "kivi_paged_append")
 
 
@@ -407,7 +415,7 @@ def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Causal attention of packed prompts: q [rows][Hq][D], k and v [rows][Hkv][D] (bf16 or fp16),
     request b in rows offsets[b] .. offsets[b+1]-1 (int32, on the device) -> out like q.  Rows
     behind the last request are left as they were."""
-    _one_device(q, k, v, offsets, workspace, out)
+    dev = _one_device(q, k, v, offsets, workspace, out)
     if out is None:
         out = _new_out(q, stream)
     rows, hq, dim = q.shape
@@ -422,7 +430,7 @@ def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         _row_stride(v, "v"), out.data_ptr(), _row_stride(out, "out"), _DTYPES[q.dtype],
         _int_array(offsets, (B + 1,), "offsets"), B, rows, hkv, hq, dim, float(sm_scale),
         _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)), "kivi_packed_attention")
+        _stream_on(dev, stream)), "kivi_packed_attention")
     return out
 
 
@@ -435,7 +443,7 @@ def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     offsets[b+1]-1) over its kv_lengths[b] keys in the pages of block_table[b], causal, the new
     tokens being the last keys -> out like q.  max_new: no request has more new rows (1 in a
     decode step; by default the number of rows)."""
-    _one_device(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, out)
+    dev = _one_device(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, out)
     if out is None:
         out = _new_out(q, stream)
     rows, hq, dim = q.shape
@@ -450,7 +458,7 @@ def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
         _int_array(kv_lengths, (B,), "kv_lengths"), _int_array(offsets, (B + 1,), "offsets"), B,
         rows, max(rows, 1) if max_new is None else int(max_new), pages, page, hkv, hq, dim,
         float(sm_scale), _ptr(workspace, name="workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "kivi_paged_attention")
+        workspace.numel() * workspace.element_size(), _stream_on(dev, stream)), "kivi_paged_attention")
     return out
 
 

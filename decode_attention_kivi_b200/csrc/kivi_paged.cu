@@ -13,7 +13,10 @@
 // read of F and of the table that another CTA would have written is resolved
 // from the prefix sums instead, so one cluster barrier is enough: the one
 // between the reads of the lengths and the writes of the new lengths, which may
-// be the same array.
+// be the same array.  A cluster is too few threads for the rows of a large step:
+// above kRowsHere rows a second kernel fills slots and positions from the new
+// tables, four rows per thread (65,000 rows of 500 requests: 24.5 us by the
+// cluster alone, of which the rows took 19).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -29,6 +32,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kAssignThreads = 512;
 constexpr int kAssignCluster = 8;
+constexpr int kRowsHere = 2048;
 
 // Exclusive prefix sums of three counts over the block's threads, and the totals.
 struct Counts {
@@ -71,7 +75,9 @@ __device__ __forceinline__ int find_request(const int* prefix, int B, int x) {
 }
 
 __global__ void __launch_bounds__(kAssignThreads)
-paged_assign_kernel(PagedAssignArgs a) {
+paged_assign_kernel(PagedAssignArgs a, bool rows_here) {
+  wait_for_predecessor();
+  allow_successor();  // the rows' kernel waits for this one to end
   extern __shared__ int s_mem[];
   __shared__ Counts s_warp[kAssignThreads / 32];
   int* s_len = s_mem;                 // [B]
@@ -80,7 +86,7 @@ paged_assign_kernel(PagedAssignArgs a) {
   int* s_back = s_need + a.B + 1;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int page = 1 << a.page_shift;
+  const int page = 1 << a.page_shift, rows = rows_here ? a.rows : 0;
   const long long cap = (long long)a.width << a.page_shift;
 
   Counts base{0, 0, 0};
@@ -135,7 +141,7 @@ paged_assign_kernel(PagedAssignArgs a) {
       a.offsets[b] = 0;
     }
     if (tid == 0) a.offsets[a.B] = 0;
-    for (int i = tid; i < a.rows; i += step) {
+    for (int i = tid; i < rows; i += step) {
       a.slots[i] = -1;
       a.positions[i] = 0;
     }
@@ -164,7 +170,7 @@ paged_assign_kernel(PagedAssignArgs a) {
     const int have = (s_len[b] + page - 1) >> a.page_shift;
     a.table[(long)b * a.width + have + (j - s_need[b])] = stack((int)top - 1 - j);
   }
-  for (int i = tid; i < a.rows; i += step) {
+  for (int i = tid; i < rows; i += step) {
     int slot = -1, pos = 0;
     if (i < base.tok) {
       const int b = find_request(s_tok, a.B, i);
@@ -180,12 +186,38 @@ paged_assign_kernel(PagedAssignArgs a) {
   }
 }
 
+// Slots and positions of a step whose tables, lengths and offsets are made.
+__global__ void __launch_bounds__(256)
+paged_rows_kernel(PagedAssignArgs a) {
+  wait_for_predecessor();
+  const long first = 4 * ((long)blockIdx.x * blockDim.x + threadIdx.x);
+  if (first >= a.rows) return;
+  const int i0 = (int)first, n = a.rows - i0 < 4 ? a.rows - i0 : 4, page = 1 << a.page_shift;
+  const int total = a.offsets[a.B];
+  // the request of the first row, and from there on the next ones
+  int b = i0 < total ? find_request(a.offsets, a.B, i0) : a.B;
+  for (int x = 0; x < n; ++x) {
+    const int i = i0 + x;
+    int slot = -1, pos = 0;
+    if (i < total) {
+      while (a.offsets[b + 1] <= i) ++b;
+      pos = a.kv_lengths[b] - (a.offsets[b + 1] - i);
+      const int id = a.table[(long)b * a.width + (pos >> a.page_shift)];
+      const long long s = ((long long)id << a.page_shift) + (pos & (page - 1));
+      slot = id < 0 || s > INT_MAX ? -1 : (int)s;
+    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
+  }
+}
+
 // ---- append ----
 
 // One 16-byte vector of K and V per thread and step; a token's row of Hkv * D
 // values is contiguous in the input and one run of D values per head in its page.
 __global__ void __launch_bounds__(256)
 paged_append_kernel(PagedAppendArgs a) {
+  wait_for_predecessor();
   const int vec_head = a.D / 8, vec_row = a.Hkv * vec_head;
   const long total = (long)a.T * vec_row;
   for (long x = (long)blockIdx.x * blockDim.x + threadIdx.x; x < total;
@@ -224,20 +256,25 @@ cudaError_t launch_paged_assign(const PagedAssignArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(kAssignThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_assign_kernel, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  cfg.numAttrs = 2;
+  const bool rows_here = a.rows <= kRowsHere;
+  e = cudaLaunchKernelEx(&cfg, paged_assign_kernel, a, rows_here);
+  if (e != cudaSuccess || rows_here) return e;
+  return launch_pdl(paged_rows_kernel, dim3((unsigned)((a.rows + 1023L) / 1024)), dim3(256), 0, stream,
+                    a);
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   const long total = (long)a.T * a.Hkv * (a.D / 8);
   const long blocks = (total + 255) / 256;
-  paged_append_kernel<<<(unsigned)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(paged_append_kernel, dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16)),
+                    dim3(256), 0, stream, a);
 }
 
 }  // namespace kivi
