@@ -66,8 +66,8 @@ kivi_status attention_args(kivi::VarlenAttnArgs& a, int32_t dtype, const void* q
   if (!vec_array(q) || !vec_array(out) || !stride_ok(q_stride, hq, D) ||
       !stride_ok(out_stride, hq, D))
     return KIVI_ERR_INVALID_ARG;
-  // (row, head) pairs are counted in int
-  if ((int64_t)rows * hq > INT32_MAX) return KIVI_ERR_INVALID_ARG;
+  // (row, head) pairs are counted in int, rounded up to an item
+  if ((int64_t)rows * hq > INT32_MAX - 512) return KIVI_ERR_INVALID_ARG;
   a.q = q;
   a.out = out;
   a.q_stride = q_stride;

@@ -61,15 +61,18 @@ constexpr int kTileV = 128;            // keys per tile
 constexpr int kUnit = 64;              // keys of a score buffer
 constexpr int kSoftWarpsV = 8;
 constexpr int kProducerWarpV = kSoftWarpsV, kMmaWarpV = kSoftWarpsV + 1;  // and + 2: by half
-constexpr int kThreadsV = (kSoftWarpsV + 4) * 32;  // three warpgroups; one warp of the last idle
+constexpr int kPlanWarpV = kMmaWarpV + 2;
+constexpr int kThreadsV = (kSoftWarpsV + 4) * 32;  // three warpgroups
 // Registers per thread at launch, and after the softmax warpgroups took what the third gave up.
 constexpr int kRegsV = 168, kRegsSoft = 208, kRegsRest = 88;
 static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegsV, "a larger sum would wait forever");
+constexpr int kPieces = 4;             // pieces planned ahead
+constexpr int kPieceReaders = 3 + kSoftWarpsV;
 constexpr int kSlabV = 128 * 128;      // 128 rows of 64 channels
 constexpr int kSlots = 4;              // K and V tiles in flight
 constexpr uint32_t kTmemColsV = 512;
-constexpr int kMinTilesV = 4;          // tiles per CTA at least
-constexpr int kItemCost = 1;           // tiles that an item's start and end are worth
+constexpr int kMinTilesV = 2;          // tiles per CTA at least
+constexpr int kItemCost = 2;           // tiles that an item's start and end are worth
 constexpr int kChunk = 32;             // scores turned into weights at a time
 // log2 growth of a row maximum before O is rescaled: the weights stay below 2^kSlack, far inside
 // what the type and the 32-bit sums hold, and a larger slack costs no accuracy (the roundings are
@@ -87,7 +90,8 @@ struct VCfg {
   static constexpr int kTileBytes = kSlabs * kSlabV;
   static constexpr int kOffRing = 2 * kTileBytes;  // after the two halves of Q
   static constexpr int kOffBars = kOffRing + kSlots * kTileBytes;
-  static constexpr int kOffPrefix = kOffBars + 256;
+  static constexpr int kOffPieces = kOffBars + 384;
+  static constexpr int kOffPrefix = kOffPieces + kPieces * 64;
   static constexpr int kWarpState = 32 * (D + 2);  // O [D/4][32] float4, m [32], l [32]
   static constexpr int kState = kSoftWarpsV * kWarpState;
   static constexpr uint32_t kColO = 2 * kTileV;
@@ -100,18 +104,28 @@ struct VCfg {
   static_assert(kColO + 2 * D <= kTmemColsV, "TMEM plan");
 };
 
+// Query heads per kv head, and tile rows to tokens.
+struct Heads {
+  int n, shift;  // shift: log2 n, or -1
+  __device__ __forceinline__ int token(int row) const { return shift >= 0 ? row >> shift : row / n; }
+};
+
+__device__ __forceinline__ Heads heads_of(int hpk) {
+  return {hpk, (hpk & (hpk - 1)) == 0 ? __popc(hpk - 1) : -1};
+}
+
 // Units that the half of rows row0 .. row0 + 127 of an item sees; at least one where it has rows.
-__device__ __forceinline__ int half_units(const Request& r, int rows, int row0, int hpk) {
+__device__ __forceinline__ int half_units(const Request& r, int rows, int row0, const Heads& h) {
   if (row0 >= rows) return 0;
-  const int kmax = min(last_key(r, (min(row0 + kHalf, rows) - 1) / hpk), r.L - 1);
+  const int kmax = min(last_key(r, h.token(min(row0 + kHalf, rows) - 1)), r.L - 1);
   return kmax < 0 ? 1 : kmax / kUnit + 1;
 }
 constexpr int kUnits = kTileV / kUnit;
 __device__ __forceinline__ int tiles_of_units(int n) { return (n + kUnits - 1) / kUnits; }
 // Tiles of an item: those of its last rows, which see the most keys.
-__device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, int hpk) {
+__device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, const Heads& h) {
   if (tt * 2 * kHalf >= rows) return 0;
-  const int kmax = min(last_key(r, (min((tt + 1) * 2 * kHalf, rows) - 1) / hpk), r.L - 1);
+  const int kmax = min(last_key(r, h.token(min((tt + 1) * 2 * kHalf, rows) - 1)), r.L - 1);
   return kmax < 0 ? 1 : kmax / kTileV + 1;
 }
 
@@ -125,12 +139,19 @@ struct Ranges {
 };
 
 // A CTA's piece of an item: tiles j0 .. j1 - 1 of nt, for half i the units kUnits * j0 .. ei - 1.
-struct Piece {
-  int t0;  // where the item's tiles begin in the whole call, behind its cost
-  int b, kvh, tt, rows, j0, j1, nt, e0, e1;
-  Request r;
+// j1 < 0 ends the list.
+struct alignas(16) Piece {
+  int b, kvh, row0, rows;  // request, kv head, first row and number of rows of the request's heads
+  int q0, n, L;            // the request
+  int t0;                  // where the item's tiles begin in the whole call, behind its cost
+  int j0, j1, nt;
+  int u;                   // tiles of the pieces before, K and V counted
+  int e0, e1, pad[2];
+  __device__ __forceinline__ Request request() const { return {q0, n, L}; }
   __device__ __forceinline__ int end(int half) const { return half ? e1 : e0; }
+  __device__ __forceinline__ bool active(int half) const { return end(half) > kUnits * j0; }
 };
+static_assert(sizeof(Piece) == 64, "a piece is four vectors");
 
 __device__ __forceinline__ float exp2_in_order(float x) {
   float y;
@@ -222,14 +243,17 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   uint64_t* s_full = q_full + 2;      // [4], by half and buffer
   uint64_t* p_full = s_full + 4;      // [4]
   uint64_t* o_done = p_full + 4;      // [4], the product of the buffer's weights
-  uint64_t* drained = o_done + 4;
+  uint64_t* piece_full = o_done + 4;  // [kPieces]
+  uint64_t* piece_empty = piece_full + kPieces;
+  uint64_t* drained = piece_empty + kPieces;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
   int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, kvh, tt, t0 of the CTA's first item
   int* s_sum = s_start + 4;                           // [kThreadsV / 32]
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hpk = a.Hq / a.Hkv;
+  const Heads heads = heads_of(a.Hq / a.Hkv);
+  const int hpk = heads.n;
 
   if (threadIdx.x == 0) {
     *s_abort = 0;
@@ -239,6 +263,10 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], kHalf);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], kPieceReaders);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -269,14 +297,14 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     const int rows = r.n * hpk, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
     long long v = 0;
     if (items <= 4)
-      for (int tt = 0; tt < items; ++tt) v += kItemCost + item_tiles(r, rows, tt, hpk);
+      for (int tt = 0; tt < items; ++tt) v += kItemCost + item_tiles(r, rows, tt, heads);
     // requests of many items: the warp's lanes share them
     for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
       const int from = __ffs(left) - 1;
       const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
       const int rrows = rr.n * hpk;
       long long sum = 0;
-      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += kItemCost + item_tiles(rr, rrows, tt, hpk);
+      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += kItemCost + item_tiles(rr, rrows, tt, heads);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == from) v = sum;
@@ -324,88 +352,62 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       t_end = sp.lo(cta + 1);
     }
   }
-  if (warp == 0 && t_begin < t_end) {
-    int lo = 0, hi = a.B;  // largest b with prefix[b] <= t_begin
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= t_begin) lo = mid;
-      else hi = mid;
-    }
+  // the request and the item that hold t_begin, found by all threads
+  if (t_begin < t_end) {
+    for (int b = threadIdx.x; b < a.B; b += kThreadsV)
+      if (prefix[b] <= t_begin && t_begin < prefix[b + 1]) s_start[0] = b;
+    __syncthreads();
+    const int b = s_start[0];
     bool bad;
-    const Request r = load_request(a, lo, &bad);
-    const int rows = r.n * hpk, per_head = (prefix[lo + 1] - prefix[lo]) / a.Hkv;
-    const int kvh = (t_begin - prefix[lo]) / per_head;
-    int x = t_begin - prefix[lo] - kvh * per_head;  // tiles to pass within the head
-    for (int t0 = 0;; t0 += 32) {
-      const int v = kItemCost + item_tiles(r, rows, t0 + lane, hpk);
+    const Request r = load_request(a, b, &bad);
+    const int rows = r.n * hpk, items = (rows - 1) / (2 * kHalf) + 1;
+    const int per_head = (prefix[b + 1] - prefix[b]) / a.Hkv;
+    const int kvh = (t_begin - prefix[b]) / per_head;
+    int x = t_begin - prefix[b] - kvh * per_head;  // tiles to pass within the head
+    for (int i0 = 0; i0 < items; i0 += kThreadsV) {
+      const int tt = i0 + threadIdx.x, v = tt < items ? kItemCost + item_tiles(r, rows, tt, heads) : 0;
       int inc = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += o;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, inc > x);
-      if (past) {
-        if (lane == __ffs(past) - 1) {
-          s_start[0] = lo;
-          s_start[1] = kvh;
-          s_start[2] = t0 + lane;
-          s_start[3] = t_begin - (x - (inc - v)) + kItemCost;
-        }
-        break;
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = inc;
+      __syncthreads();
+      int all = 0;
+#pragma unroll
+      for (int w = 0; w < kThreadsV / 32; ++w) {
+        if (w < warp) inc += s_sum[w];
+        all += s_sum[w];
       }
-      x -= __shfl_sync(0xffffffffu, inc, 31);
+      if (v > 0 && inc - v <= x && x < inc) {
+        s_start[1] = kvh;
+        s_start[2] = tt;
+        s_start[3] = t_begin - (x - (inc - v)) + kItemCost;
+      }
+      if (x < all) break;
+      x -= all;
     }
   }
   __syncthreads();
 
-  auto set_item = [&](Piece& p) {
-    const int row0 = p.tt * 2 * kHalf;
-    p.nt = item_tiles(p.r, p.rows, p.tt, hpk);
-    p.j0 = max(0, t_begin - p.t0);
-    p.j1 = min(p.nt, t_end - p.t0);
-    p.e0 = min(half_units(p.r, p.rows, row0, hpk), kUnits * p.j1);
-    p.e1 = min(half_units(p.r, p.rows, row0 + kHalf, hpk), kUnits * p.j1);
-  };
-  auto set_request = [&](Piece& p, int b) {
-    bool bad;
-    p.b = b;
-    p.r = load_request(a, b, &bad);
-    p.rows = p.r.n * hpk;
-  };
-  auto first_piece = [&]() {
-    Piece p;
-    p.t0 = t_end;
-    if (t_begin < t_end) {
-      set_request(p, s_start[0]);
-      p.kvh = s_start[1];
-      p.tt = s_start[2];
-      p.t0 = s_start[3];
-      set_item(p);
-    }
-    return p;
-  };
-  // the piece after p; it is there if its t0 < t_end
-  auto next_piece = [&](Piece& p) {
-    p.t0 += p.nt + kItemCost;
-    if (p.t0 >= t_end) return;
-    if (++p.tt * 2 * kHalf >= p.rows) {
-      p.tt = 0;
-      if (++p.kvh == a.Hkv) {
-        p.kvh = 0;
-        int b = p.b + 1;
-        while (prefix[b + 1] == prefix[b]) ++b;
-        set_request(p, b);
-      }
-    }
-    set_item(p);
-  };
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::kOffPieces);
   auto fail = [&]() {
     *s_abort = 1;
     atomicOr(a.status, kPagedTimeout);
   };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, s_abort); };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, s_abort));
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+  // piece k of the CTA, read by a whole warp; false where the wait ran out
+  auto read_piece = [&](int k, Piece& p) {
+    if (!wait_warp(&piece_full[k % kPieces], (uint32_t)(k / kPieces) & 1u)) return false;
+    p = pieces[k % kPieces];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[k % kPieces]);
+    return true;
   };
 
   if (warp < kSoftWarpsV) {
@@ -417,9 +419,9 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     unsigned char* qs = smem + hf * C::kTileBytes;
     // starts the copies of the half's Q rows (a row is 2 D bytes, D / 8 lanes to a row)
     auto fetch_q = [&](const Piece& p) {
-      const int row = p.tt * 2 * kHalf + hf * kHalf + r, i = row / hpk;
+      const int row = p.row0 + hf * kHalf + r, i = heads.token(row);
       const bool real = row < p.rows;
-      const long off = real ? (p.r.q0 + i) * a.q_stride + (long)(p.kvh * hpk + row - i * hpk) * D : -1;
+      const long off = real ? (p.q0 + i) * a.q_stride + (long)(p.kvh * hpk + row - i * hpk) * D : -1;
       constexpr int kPer = D / 8, kStep = 32 / kPer;  // lanes per row, rows per step
       const int c = lane % kPer, first = (warp & 3) * 32;
 #pragma unroll 4
@@ -440,26 +442,25 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       fence_proxy_async();  // Q is read by the tensor cores
       mbar_arrive(&q_full[hf]);
     };
+    const bool wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
     uint32_t ns = 0;  // phases by buffer: bit b is that of its next scores, its last product had the other
-    int u = 0;  // tiles of the pieces before, as the producer counts them
-    bool ok = true;
     Cut cut{0, 0, 0, 0, 0, {0, 0, 0}};
-    Piece p = first_piece();
-    if (p.t0 < t_end && p.end(hf) > kUnits * p.j0) {
+    Piece p, nx;  // the next piece is read during the last unit of this one
+    int k = 0;
+    bool ok = read_piece(k++, p);
+    if (ok && p.j1 >= 0 && p.active(hf)) {
       fetch_q(p);
       q_here();
     }
-    while (ok && p.t0 < t_end) {
-      Piece nx = p;
-      next_piece(nx);
+    while (ok && p.j1 >= 0) {
       const int n0 = kUnits * p.j0, e = p.end(hf);
-      const bool more = nx.t0 < t_end && nx.end(hf) > kUnits * nx.j0;
       const bool active = e > n0;
-      const int row = p.tt * 2 * kHalf + hf * kHalf + r, qi = row / hpk;
+      const Request req = p.request();
+      const int row = p.row0 + hf * kHalf + r, qi = heads.token(row);
       const bool real = row < p.rows;
-      const int last = real ? min(last_key(p.r, qi), p.r.L - 1) : -1;
+      const int last = real ? min(last_key(req, qi), req.L - 1) : -1;
       // units that end behind this key need the mask
-      const int clear = min(last_key(p.r, (row - r) / hpk), p.r.L - 1);
+      const int clear = min(last_key(req, heads.token(row - r)), req.L - 1);
       float m = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
       for (int n = n0; n < e; ++n) {
         const int buf = n % kUnits;
@@ -467,14 +468,17 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
         if (!(ok = wait_warp(&s_full[2 * hf + buf], ns >> buf & 1u))) break;
         ns ^= 1u << buf;
         tc::fence_after();
-        if (more && n + 1 == e) fetch_q(nx);  // this item's scores are done with Q
+        if (n + 1 == e) {  // this item's scores are done with Q
+          if (!(ok = read_piece(k++, nx))) break;
+          if (nx.j1 >= 0 && nx.active(hf)) fetch_q(nx);
+        }
         float s[kUnit];
         tc::ld_x64(col, s);
-        const int nv = p.r.L - n / kUnits * kTileV;  // keys of the tile
+        const int nv = req.L - n / kUnits * kTileV;  // keys of the tile
         if (buf == 0 && nv > 0 && nv < kTileV && (nv & 15)) {
           // V rows behind the last key up to a whole step: a weight of 0 times NaN (both halves
           // write the zeros)
-          const int x = u + 2 * (n / kUnits - p.j0) + 1;
+          const int x = p.u + (n - n0) / kUnits * 2 + 1;
           if (!(ok = wait_warp(&full[x % kSlots], (uint32_t)(x / kSlots) & 1u))) break;
           unsigned char* vs = smem + C::kOffRing + (x % kSlots) * C::kTileBytes;
           for (int y = r; y < (16 - (nv & 15)) * C::kSlabs * 8; y += kHalf) {
@@ -527,17 +531,21 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
         mbar_arrive(&p_full[2 * hf + buf]);
       }
       if (!ok) break;
-      if (!active && more) fetch_q(nx);
-      if (more) q_here();
+      if (!active) {
+        if (!(ok = read_piece(k++, nx))) break;
+        if (nx.j1 >= 0 && nx.active(hf)) fetch_q(nx);
+      }
+      if (nx.j1 >= 0 && nx.active(hf)) q_here();
       if (active) {
         const int buf = (e - 1) % kUnits;
         if (!(ok = wait_warp(&o_done[2 * hf + buf], ~ns >> buf & 1u))) break;
         tc::fence_after();
       }
-      T* dst = static_cast<T*>(a.out) + (p.r.q0 + (real ? qi : 0)) * a.out_stride +
+      T* dst = static_cast<T*>(a.out) + (p.q0 + (real ? qi : 0)) * a.out_stride +
                (long)(p.kvh * hpk + (real ? row - qi * hpk : 0)) * D;
       if (p.j0 == 0 && p.j1 == p.nt) {
         if (active) {
+          // a store touches a line per lane whatever its width: 32 bytes of the row where it is aligned
           const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -545,58 +553,114 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             tc::ld_x32(col_o + c0, o);
             if (real)
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)  // no product was made where no key is seen
+                for (int x = 0; x < 8; ++x)  // no product was made where no key is seen
                   w[x] = l > 0.f ? Elem<T>::pack(o[i + 2 * x] * inv, o[i + 2 * x + 1] * inv) : 0u;
-                *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (wide_out) {
+                  store_32_bytes(dst + c0 + i, w);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4*>(dst + c0 + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
               }
           }
         }
-      } else if (p.tt * 2 * kHalf + (warp >> 2) * kHalf + (warp & 3) * 32 < p.rows) {
-        // slot 0: the item this CTA begins in the middle of; slot 1: the one it leaves unfinished
-        float* part = partial_of<D>(a, cta, p.j0 > 0 ? 0 : 1) + warp * C::kWarpState;
-        if (active) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tc::ld_x32(col_o + c0, o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(part)[(c0 / 4 + i) * 32 + lane] =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-        }
-        part[32 * D + lane] = m;
-        part[32 * (D + 1) + lane] = l;
+      } else {
         const int c0 = sp.cta_of(p.t0), c1 = sp.cta_of(p.t0 + p.nt - 1);
-        if (join_here) {
-          __threadfence();
-          __syncwarp();
-          int* ticket = a.tickets + c0 * kTickets + warp;
-          int arrived = 0;
-          if (lane == 0) arrived = atomicAdd(ticket, 1);
-          if (__shfl_sync(0xffffffffu, arrived, 0) == c1 - c0) {
-            __threadfence();
-            join_rows<T, D, D / 4>(
-                c1 - c0 + 1,
-                [&](int w) { return partial_of<D>(a, c0 + w, w == 0 ? 1 : 0) + warp * C::kWarpState; },
-                lane, 0, real, dst);
-            if (lane == 0) *ticket = 0;  // ready for the next call
+        if (p.j0 == 0) cut = Cut{c1 - c0 + 1, p.q0, p.kvh, p.row0, p.rows, {0, 0, 0}};
+        if (p.row0 + warp * 32 < p.rows) {
+          // slot 0: the item this CTA begins in the middle of; slot 1: the one it leaves unfinished
+          float* part = partial_of<D>(a, cta, p.j0 > 0 ? 0 : 1) + warp * C::kWarpState;
+          if (active) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tc::ld_x32(col_o + c, o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(part)[(c / 4 + i) * 32 + lane] =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           }
-        } else if (p.j0 == 0) {
-          cut = Cut{c1 - c0 + 1, p.r.q0, p.kvh, p.tt * 2 * kHalf, p.rows, {0, 0, 0}};
+          part[32 * D + lane] = m;
+          part[32 * (D + 1) + lane] = l;
+          if (join_here) {
+            __threadfence();
+            __syncwarp();
+            int* ticket = a.tickets + c0 * kTickets + warp;
+            int arrived = 0;
+            if (lane == 0) arrived = atomicAdd(ticket, 1);
+            if (__shfl_sync(0xffffffffu, arrived, 0) == c1 - c0) {
+              __threadfence();
+              join_rows<T, D, D / 4>(
+                  c1 - c0 + 1,
+                  [&](int x) { return partial_of<D>(a, c0 + x, x == 0 ? 1 : 0) + warp * C::kWarpState; },
+                  lane, 0, real, dst);
+              if (lane == 0) *ticket = 0;  // ready for the next call
+            }
+          }
         }
       }
-      u += 2 * (p.j1 - p.j0);
       p = nx;
     }
     if (!ok) fail();
     if (!join_here && threadIdx.x == 0) reinterpret_cast<Cut*>(a.partials)[cta] = cut;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == kProducerWarpV) {
+    if (warp == kPlanWarpV) {
+      // ---- plan: the CTA's pieces, by one lane ----
+      if (lane == 0) {
+        bool ok = true, bad;
+        int k = 0, u = 0, t0 = t_end;
+        Piece p{};
+        Request r{0, 0, 0};
+        if (t_begin < t_end) {
+          p.b = s_start[0];
+          p.kvh = s_start[1];
+          p.row0 = s_start[2] * 2 * kHalf;
+          t0 = s_start[3];
+          r = load_request(a, p.b, &bad);
+        }
+        for (;; ++k) {
+          ok = k < kPieces || wait(&piece_empty[k % kPieces], (uint32_t)(k / kPieces - 1) & 1u);
+          if (!ok) break;
+          const bool more = t0 < t_end;
+          p.j1 = -1;
+          if (more) {
+            p.rows = r.n * hpk;
+            p.q0 = r.q0;
+            p.n = r.n;
+            p.L = r.L;
+            p.t0 = t0;
+            p.nt = item_tiles(r, p.rows, p.row0 / (2 * kHalf), heads);
+            p.j0 = max(0, t_begin - t0);
+            p.j1 = min(p.nt, t_end - t0);
+            p.u = u;
+            p.e0 = min(half_units(r, p.rows, p.row0, heads), kUnits * p.j1);
+            p.e1 = min(half_units(r, p.rows, p.row0 + kHalf, heads), kUnits * p.j1);
+          }
+          pieces[k % kPieces] = p;
+          mbar_arrive(&piece_full[k % kPieces]);
+          if (!more) break;
+          u += 2 * (p.j1 - p.j0);
+          t0 += p.nt + kItemCost;
+          if (t0 >= t_end) continue;
+          p.row0 += 2 * kHalf;
+          if (p.row0 >= p.rows) {
+            p.row0 = 0;
+            if (++p.kvh == a.Hkv) {
+              p.kvh = 0;
+              ++p.b;
+              while (prefix[p.b + 1] == prefix[p.b]) ++p.b;
+              r = load_request(a, p.b, &bad);
+            }
+          }
+        }
+        if (!ok) fail();
+      }
+    } else if (warp == kProducerWarpV) {
       // ---- producer: tiles u = 2 s (K) and 2 s + 1 (V) of the CTA's step s, slot u mod 4 ----
       const int box = PAGED ? min(1 << a.page_shift, kTileV) : kTileV;
       const int boxes = kTileV / box * C::kSlabs;  // of a tile, one per lane (at most 16)
@@ -604,10 +668,11 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       const int outside = PAGED ? (a.num_pages * a.Hkv) << a.page_shift : 0;  // rows of zeros
       int u = 0;
       bool ok = true;
-      for (Piece p = first_piece(); ok && p.t0 < t_end; next_piece(p)) {
+      Piece p;
+      for (int k = 0; ok && (ok = read_piece(k, p)) && p.j1 >= 0; ++k) {
         for (int j = p.j0; ok && j < p.j1; ++j) {
           const int key = j * kTileV + part * box;
-          const bool mine = lane < boxes && key < p.r.L;
+          const bool mine = lane < boxes && key < p.L;
           int x = 64 * slab, y = 0;
           if (PAGED) {
             y = outside;
@@ -620,7 +685,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             }
           } else {
             x += p.kvh * D;
-            y = p.r.q0 + key;
+            y = p.q0 + key;
           }
           const int n = __popc(__ballot_sync(0xffffffffu, mine));
           for (int v = 0; v < 2; ++v, ++u) {
@@ -640,8 +705,6 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       // every copy issued lands before the CTA may exit
       for (int i = max(u - kSlots, 0); i < u; ++i)
         if (!mbar_wait_bounded(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u)) fail();
-    } else if (warp != kMmaWarpV && warp != kMmaWarpV + 1) {
-      // idle
     } else if (tc::elect_one()) {
       // ---- MMA of half i, by one lane ----
       const int i = warp - kMmaWarpV;
@@ -654,15 +717,17 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       const uint64_t vd = tc::desc_sw128(smem_addr(smem + C::kOffRing), kSlabV, 1024);
       const uint32_t ts = tmem + i * kTileV, to = tmem + C::kColO + i * D;
       uint32_t nq = 0, np = 0;  // phases; bit b of np: of buffer b
-      int u = 0;  // tiles of the pieces before, as the producer counts them
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, s_abort); };
       auto wait_tile = [&](int x) { return wait(&full[x % kSlots], (uint32_t)(x / kSlots) & 1u); };
-      for (Piece p = first_piece(); ok && p.t0 < t_end; next_piece(p)) {
-        const int n0 = kUnits * p.j0, e = p.end(i);
+      for (int k = 0; ok; ++k) {
+        if (!(ok = wait(&piece_full[k % kPieces], (uint32_t)(k / kPieces) & 1u))) break;
+        const Piece p = pieces[k % kPieces];
+        mbar_arrive(&piece_empty[k % kPieces]);
+        if (p.j1 < 0) break;
+        const int n0 = kUnits * p.j0, e = p.end(i), u = p.u;
         // keys that some row of the half sees
         const int seen =
-            min(last_key(p.r, (min(p.tt * 2 * kHalf + (i + 1) * kHalf, p.rows) - 1) / hpk) + 1, p.r.L);
+            min(last_key(p.request(), heads.token(min(p.row0 + (i + 1) * kHalf, p.rows) - 1)) + 1, p.L);
         // the scores of unit n from K tile x, released behind the last unit in it
         auto scores = [&](int n, int x) {
           const uint64_t kt = kd + (x % kSlots) * kTile16 + (n % kUnits) * kUnit16;
@@ -709,7 +774,6 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             ok = wait_tile(y);
             if (ok) tc::commit(&empty[y % kSlots]);
           }
-        u += 2 * (p.j1 - p.j0);
       }
       if (!ok) fail();
       // all that was issued has completed before TMEM is released
