@@ -14,10 +14,10 @@
 // so long chunks are bound by the tensor cores and, equally, by the 128 * 256
 // exponentials of a tile (16 per SM and cycle: 2048 cycles, as long as its
 // products take).
-// The tiles of all items, in order, each item kItemCost tiles longer than it is,
-// are cut into one contiguous range per CTA, equal to within a tile whatever the
-// lengths are; every CTA forms the prefix sums that this needs from the device
-// arrays.
+// The work of all items, in order, is cut into one contiguous range per CTA,
+// equal to within a tile whatever the lengths are, an item counted as kItemCost
+// and, for each of its tiles, the units of 64 keys that its halves go through;
+// every CTA forms the prefix sums that this needs from the device arrays.
 //
 // Twelve warps (two idle), one CTA per SM:
 //   warp 8 (producer)  2D tensor copies of K and V tiles into a ring of four
@@ -71,8 +71,8 @@ constexpr int kPieceReaders = 3 + kSoftWarpsV;
 constexpr int kSlabV = 128 * 128;      // 128 rows of 64 channels
 constexpr int kSlots = 4;              // K and V tiles in flight
 constexpr uint32_t kTmemColsV = 512;
-constexpr int kMinTilesV = 2;          // tiles per CTA at least
-constexpr int kItemCost = 2;           // tiles that an item's start and end are worth
+constexpr int kMinWorkV = 8;           // half-units per CTA at least
+constexpr int kItemCost = 8;           // half-units that an item's start and end take as long as
 constexpr int kChunk = 32;             // scores turned into weights at a time
 // log2 growth of a row maximum before O is rescaled: the weights stay below 2^kSlack, far inside
 // what the type and the 32-bit sums hold, and a larger slack costs no accuracy (the roundings are
@@ -129,8 +129,16 @@ __device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, co
   return kmax < 0 ? 1 : kmax / kTileV + 1;
 }
 
+// Work of a tile of the item (both halves' units, or the one half's), and of an item.
+__device__ __forceinline__ int tile_work(int rows, int row0) {
+  return rows - row0 > kHalf ? 2 * kUnits : kUnits;
+}
+__device__ __forceinline__ int item_work(const Request& r, int rows, int tt, const Heads& h) {
+  return kItemCost + item_tiles(r, rows, tt, h) * tile_work(rows, tt * 2 * kHalf);
+}
+
 struct Ranges {
-  int n, q, rem;  // CTAs with work; total = n * q + rem
+  int n, q, rem;  // CTAs with work; total = n * q + rem, q at least a tile where n > 1
   __device__ __forceinline__ int lo(int c) const { return c * q + min(c, rem); }
   __device__ __forceinline__ int cta_of(int t) const {
     const int big = rem * (q + 1);
@@ -143,10 +151,10 @@ struct Ranges {
 struct alignas(16) Piece {
   int b, kvh, row0, rows;  // request, kv head, first row and number of rows of the request's heads
   int q0, n, L;            // the request
-  int t0;                  // where the item's tiles begin in the whole call, behind its cost
+  int t0, w;               // where the item's tiles begin in the call's work, and the work of one
   int j0, j1, nt;
   int u;                   // tiles of the pieces before, K and V counted
-  int e0, e1, pad[2];
+  int e0, e1, pad;
   __device__ __forceinline__ Request request() const { return {q0, n, L}; }
   __device__ __forceinline__ int end(int half) const { return half ? e1 : e0; }
   __device__ __forceinline__ bool active(int half) const { return end(half) > kUnits * j0; }
@@ -297,14 +305,14 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     const int rows = r.n * hpk, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
     long long v = 0;
     if (items <= 4)
-      for (int tt = 0; tt < items; ++tt) v += kItemCost + item_tiles(r, rows, tt, heads);
+      for (int tt = 0; tt < items; ++tt) v += item_work(r, rows, tt, heads);
     // requests of many items: the warp's lanes share them
     for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
       const int from = __ffs(left) - 1;
       const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
       const int rrows = rr.n * hpk;
       long long sum = 0;
-      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += kItemCost + item_tiles(rr, rrows, tt, heads);
+      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_work(rr, rrows, tt, heads);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == from) v = sum;
@@ -344,7 +352,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   Ranges sp{0, 0, 0};
   int t_begin = 0, t_end = 0;
   if (fits && base > 0) {
-    sp.n = min((int)gridDim.x, (int)((base + kMinTilesV - 1) / kMinTilesV));
+    sp.n = min((int)gridDim.x, (int)((base + kMinWorkV - 1) / kMinWorkV));
     sp.q = (int)base / sp.n;
     sp.rem = (int)base - sp.n * sp.q;
     if (cta < sp.n) {
@@ -363,9 +371,9 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     const int rows = r.n * hpk, items = (rows - 1) / (2 * kHalf) + 1;
     const int per_head = (prefix[b + 1] - prefix[b]) / a.Hkv;
     const int kvh = (t_begin - prefix[b]) / per_head;
-    int x = t_begin - prefix[b] - kvh * per_head;  // tiles to pass within the head
+    int x = t_begin - prefix[b] - kvh * per_head;  // work to pass within the head
     for (int i0 = 0; i0 < items; i0 += kThreadsV) {
-      const int tt = i0 + threadIdx.x, v = tt < items ? kItemCost + item_tiles(r, rows, tt, heads) : 0;
+      const int tt = i0 + threadIdx.x, v = tt < items ? item_work(r, rows, tt, heads) : 0;
       int inc = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -568,7 +576,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
           }
         }
       } else {
-        const int c0 = sp.cta_of(p.t0), c1 = sp.cta_of(p.t0 + p.nt - 1);
+        const int c0 = sp.cta_of(p.t0 + p.w - 1), c1 = sp.cta_of(p.t0 + p.nt * p.w - 1);
         if (p.j0 == 0) cut = Cut{c1 - c0 + 1, p.q0, p.kvh, p.row0, p.rows, {0, 0, 0}};
         if (p.row0 + warp * 32 < p.rows) {
           // slot 0: the item this CTA begins in the middle of; slot 1: the one it leaves unfinished
@@ -626,7 +634,9 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
         for (;; ++k) {
           ok = k < kPieces || wait(&piece_empty[k % kPieces], (uint32_t)(k / kPieces - 1) & 1u);
           if (!ok) break;
-          const bool more = t0 < t_end;
+          // tile j belongs to the CTA whose range holds the end of its work
+          const int w = tile_work(r.n * hpk, p.row0);
+          const bool more = t0 + w <= t_end;
           p.j1 = -1;
           if (more) {
             p.rows = r.n * hpk;
@@ -634,9 +644,10 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             p.n = r.n;
             p.L = r.L;
             p.t0 = t0;
+            p.w = w;
             p.nt = item_tiles(r, p.rows, p.row0 / (2 * kHalf), heads);
-            p.j0 = max(0, t_begin - t0);
-            p.j1 = min(p.nt, t_end - t0);
+            p.j0 = max(0, t_begin - t0) / w;
+            p.j1 = min(p.nt, (t_end - t0) / w);
             p.u = u;
             p.e0 = min(half_units(r, p.rows, p.row0, heads), kUnits * p.j1);
             p.e1 = min(half_units(r, p.rows, p.row0 + kHalf, heads), kUnits * p.j1);
@@ -645,7 +656,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
           mbar_arrive(&piece_full[k % kPieces]);
           if (!more) break;
           u += 2 * (p.j1 - p.j0);
-          t0 += p.nt + kItemCost;
+          t0 += p.nt * w + kItemCost;
           if (t0 >= t_end) continue;
           p.row0 += 2 * kHalf;
           if (p.row0 >= p.rows) {
