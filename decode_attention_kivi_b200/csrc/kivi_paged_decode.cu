@@ -10,8 +10,10 @@
 // every CTA from the device arrays.
 //
 // Each CTA (one per SM) has a producer warp that streams K and V through a ring
-// of stages with 2D tensor copies, one box of min(page, 64) rows x 64 channels
-// per lane, the page ids read by the lane that needs them.  Four consumer warps
+// of stages with tensor copies, one box of min(page, 64) whole rows per lane, the
+// page ids read by the lane that needs them.  A box lies in shared memory as
+// its 64-channel slabs, one behind the other, so that small pages need no more
+// than one copy each (a copy per slab took 10% longer at pages of 16).  Four consumer warps
 // take 16 keys of every tile each, on the tensor cores (mma.sync m16n8k16, fp32
 // accumulation): S[row][key] = Q K^T with Q in registers, an online softmax in
 // base 2 whose weights stay in registers as the operand of O[row][chan] += P V.
@@ -80,7 +82,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
   int* s_flag = reinterpret_cast<int*>(empty + C::kStages);  // the ticket's verdict
   volatile int* s_abort = s_flag + 1;
   volatile int* s_issued = s_flag + 2;
-  int* s_sum = s_flag + 4;  // [kWarpsD + 1] sums of the scan
+  long long* s_sum = reinterpret_cast<long long*>(s_flag + 4);  // [kWarpsD + 1] sums of the scan
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hpk = a.Hq / a.Hkv;
@@ -97,41 +99,45 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
   wait_for_predecessor();
 
   // ---- prefix sums of the requests' tiles ----
-  int base = 0;
+  long long base = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreadsD) {
     const int b = b0 + threadIdx.x;
-    int v = 0;
+    long long v = 0;
     if (b < a.B) {
       bool bad = false;
       const Request r = load_request(a, b, &bad);
       if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
-      if (r.n > 0 && is_short(r.n, hpk)) v = a.Hkv * tiles_of(r);
+      if (r.n > 0 && is_short(r.n, hpk)) v = (long long)a.Hkv * tiles_of(r);
     }
-    int inc = v;
+    long long inc = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, d);
+      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
       if (lane >= d) inc += o;
     }
     __syncthreads();
     if (lane == 31) s_sum[warp] = inc;
     __syncthreads();
-    int before = 0, all = 0;
+    long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w <= kWarpsD; ++w) {
       if (w < warp) before += s_sum[w];
       all += s_sum[w];
     }
-    if (b < a.B) prefix[b] = base + before + inc - v;
+    if (b < a.B) prefix[b] = (int)(base + before + inc - v);  // used where the total fits
     base += all;
   }
-  if (threadIdx.x == 0) prefix[a.B] = base;
+  if (threadIdx.x == 0) prefix[a.B] = (int)base;
   __syncthreads();
+  if (base > INT32_MAX) {  // more tiles than a call counts: nothing is computed
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kPagedBadLength);
+    return;
+  }
   Split sp;
-  sp.n = min((int)gridDim.x, (base + kMinTilesD - 1) / kMinTilesD);
+  sp.n = min((int)gridDim.x, (int)((base + kMinTilesD - 1) / kMinTilesD));
   if ((int)blockIdx.x >= sp.n) return;
-  sp.q = base / sp.n;
-  sp.rem = base - sp.n * sp.q;
+  sp.q = (int)base / sp.n;
+  sp.rem = (int)base - sp.n * sp.q;
   const int cta = blockIdx.x, t_begin = sp.lo(cta), n_tiles = sp.lo(cta + 1) - t_begin;
 
   auto enter = [&](Cursor& c, int b) {
@@ -171,8 +177,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // ---- producer ----
     const int page = 1 << a.page_shift, rows = page < kTileD ? page : kTileD;
     const int per_tile = kTileD / rows;           // boxes of a slab
-    const int boxes = per_tile * C::kSlabs * 2;   // of a stage, one per lane (at most 16)
-    const int is_v = lane & 1, slab = (lane >> 1) % C::kSlabs, part = (lane >> 1) / C::kSlabs;
+    const int boxes = per_tile * 2;               // of a stage, one per lane (at most 8)
+    const int is_v = lane & 1, part = lane >> 1;
     const int outside = (a.num_pages * a.Hkv) << a.page_shift;  // a row that reads as zero
     const CUtensorMap* map = is_v ? &tv : &tk;
     Cursor c = start();
@@ -201,11 +207,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       }
       const int n = __popc(__ballot_sync(0xffffffffu, mine));
       unsigned char* st = smem + s * C::kStageBytes;
-      if (lane == 0) mbar_expect_tx(&full[s], n * rows * 128);
+      if (lane == 0) mbar_expect_tx(&full[s], n * rows * 2 * D);
       __syncwarp();
       if (mine)
-        tma_load_2d(st + is_v * C::kTileBytes + slab * kBoxD + part * rows * 128, map, 64 * slab, y,
-                    &full[s]);
+        tma_load_3d(st + is_v * C::kTileBytes + part * rows * 2 * D, map, 0, y, 0, &full[s]);
       issued = i + 1;
     }
     if (lane == 0) *s_issued = issued;
@@ -216,6 +221,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
 
   // ---- consumers ----
   const int g = lane >> 2, tig = lane & 3, r0 = 16 * warp;
+  // this warp's 16 rows of a tile: where they begin, and the way from slab to slab
+  const int box_rows = min(1 << a.page_shift, kTileD), slab_bytes = box_rows * 128;
+  const int row_base = r0 / box_rows * box_rows * 2 * D + r0 % box_rows * 128;
   constexpr int kKS = D / 16, kNT = D / 8;
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   uint32_t qf[kKS][4];
@@ -256,19 +264,35 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     const int rows = c.r.n * hpk;
     for (int x = threadIdx.x; x < rows * (D / 4); x += kWarpsD * 32) {
       const int row = x / (D / 4), ch = x % (D / 4);
-      float M = -INFINITY;
-      for (int w = 0; w < count; ++w) M = fmaxf(M, ld(src(w) + kDecodeRows * D + row));
-      float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int w = 0; w < count; ++w) {
-        const float* s = src(w);
-        const float mw = ld(s + kDecodeRows * D + row);
-        const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-        L += f * ld(s + kDecodeRows * (D + 1) + row);
-        const float4 q = ld(reinterpret_cast<const float4*>(s + row * D) + ch);
-        v[0] += f * q.x;
-        v[1] += f * q.y;
-        v[2] += f * q.z;
-        v[3] += f * q.w;
+      // four states at a time: their loads are in flight together
+      float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w0 = 0; w0 < count; w0 += 4) {
+        float mw[4], lw[4];
+        float4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* s = src(min(w0 + i, count - 1));
+          mw[i] = ld(s + kDecodeRows * D + row);
+          lw[i] = ld(s + kDecodeRows * (D + 1) + row);
+          q[i] = ld(reinterpret_cast<const float4*>(s + row * D) + ch);
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mn = fmaxf(mn, mw[i]);
+        const float mu = mn == -INFINITY ? 0.f : mn, f0 = fast_exp2(M - mu);
+        M = mn;
+        L *= f0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= f0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = w0 + i < count ? fast_exp2(mw[i] - mu) : 0.f;
+          L += f * lw[i];
+          v[0] += f * q[i].x;
+          v[1] += f * q[i].y;
+          v[2] += f * q[i].z;
+          v[3] += f * q[i].w;
+        }
       }
       const float inv = L > 0.f ? 1.f / L : 0.f;  // a row without keys is 0
       const int i = row / hpk;
@@ -385,24 +409,24 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     const int nv = min(16, c.r.L - key0);
     unsigned char* st = smem + s * C::kStageBytes;
     if (nv > 0) {
-      const uint32_t kb = smem_addr(st), vb = smem_addr(st + C::kTileBytes);
+      const uint32_t kb = smem_addr(st) + row_base, vb = kb + C::kTileBytes;
       if (nv < 16) {  // keys behind the last: their V rows must be 0 (a weight of 0 times NaN)
         for (int x = lane; x < (16 - nv) * C::kSlabs * 8; x += 32) {
-          const int row = r0 + nv + x / (C::kSlabs * 8), rest = x % (C::kSlabs * 8);
-          *reinterpret_cast<uint4*>(st + C::kTileBytes + (rest / 8) * kBoxD + row * 128 +
-                                    16 * (rest % 8)) = make_uint4(0u, 0u, 0u, 0u);
+          const int row = nv + x / (C::kSlabs * 8), rest = x % (C::kSlabs * 8);
+          *reinterpret_cast<uint4*>(st + C::kTileBytes + row_base + (rest / 8) * slab_bytes +
+                                    row * 128 + 16 * (rest % 8)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async();  // the stage's next tensor copy comes after these writes
         __syncwarp();
       }
       // ---- scores ----
       float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const int krow = r0 + (lane & 7) + 8 * (lane >> 4);
+      const int krow = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         const int ch = 16 * ks + 8 * ((lane >> 3) & 1);
         uint32_t kf[4];
-        ldsm_x4(kf, kb + (ch / 64) * kBoxD + krow * 128 + ((((ch % 64) >> 3) ^ (krow & 7)) << 4));
+        ldsm_x4(kf, kb + (ch / 64) * slab_bytes + krow * 128 + ((((ch % 64) >> 3) ^ (krow & 7)) << 4));
         Elem<T>::mma(sa[0], qf[ks], kf[0], kf[1]);
         Elem<T>::mma(sa[1], qf[ks], kf[2], kf[3]);
       }
@@ -440,13 +464,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         }
       }
       // ---- P V ----
-      const int vrow = r0 + (lane & 7) + 8 * ((lane >> 3) & 1);
+      const int vrow = (lane & 7) + 8 * ((lane >> 3) & 1);
 #pragma unroll
       for (int n2 = 0; n2 < kNT / 2; ++n2) {
         const int ch = 16 * n2 + 8 * (lane >> 4);
         uint32_t vf[4];
         ldsm_x4_trans(vf,
-                      vb + (ch / 64) * kBoxD + vrow * 128 + ((((ch % 64) >> 3) ^ (vrow & 7)) << 4));
+                      vb + (ch / 64) * slab_bytes + vrow * 128 + ((((ch % 64) >> 3) ^ (vrow & 7)) << 4));
         Elem<T>::mma(o[2 * n2], p, vf[0], vf[1]);
         Elem<T>::mma(o[2 * n2 + 1], p, vf[2], vf[3]);
       }
@@ -481,7 +505,7 @@ cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t str
   const long rows = ((long)a.num_pages * a.Hkv) << a.page_shift;
   const int box = a.page_shift < 6 ? 1 << a.page_shift : kTileD;
   CUtensorMap tk, tv;
-  if (!encode_bf16_map(&tk, a.k, rows, D, box) || !encode_bf16_map(&tv, a.v, rows, D, box))
+  if (!encode_bf16_slabs_map(&tk, a.k, rows, D, box) || !encode_bf16_slabs_map(&tv, a.v, rows, D, box))
     return cudaErrorInvalidValue;
   const int grid = a.num_sms < kMaxGrid ? a.num_sms : kMaxGrid;
   e = launch_pdl(paged_decode_kernel<T, D>, dim3(grid), dim3(kThreadsD), C::bytes(a.B), stream, tk,
