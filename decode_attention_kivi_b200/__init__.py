@@ -319,14 +319,14 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return heads * dim if t.shape[0] < 2 else row
 
 
-def _new_out(q: torch.Tensor, stream) -> torch.Tensor:
-    """An output of q's shape that belongs to the stream the call runs on."""
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _int_array(t: torch.Tensor, shape, name: str) -> int:
@@ -417,7 +417,7 @@ def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     behind the last request are left as they were."""
     dev = _one_device(q, k, v, offsets, workspace, out)
     if out is None:
-        out = _new_out(q, stream)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     rows, hq, dim = q.shape
     hkv = k.shape[1]
     if k.shape != (rows, hkv, dim) or v.shape != k.shape or out.shape != q.shape:
@@ -445,7 +445,7 @@ def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     decode step; by default the number of rows)."""
     dev = _one_device(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, out)
     if out is None:
-        out = _new_out(q, stream)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     rows, hq, dim = q.shape
     pages, hkv, page, pdim = _pages(k_pages, v_pages, q.dtype)
     if pdim != dim or out.shape != q.shape or out.dtype != q.dtype or block_table.dim() != 2:
@@ -499,6 +499,7 @@ class PagedCache:
         self.num_free = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
         self.offsets = torch.zeros(max_requests + 1, dtype=torch.int32, device=dev)
         self.slots = self.positions = torch.zeros(0, dtype=torch.int32, device=dev)
+        self._rows = {}  # slots and positions of each number of rows that a step has had
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.workspace = torch.zeros(n, dtype=torch.uint8, device=dev)
         self.max_new = 1
@@ -507,9 +508,11 @@ class PagedCache:
                stream=None) -> None:
         """Starts a step: new_tokens [max_requests] (int32, device; negative releases), `rows`
         packed rows in the step's buffers, of which no request has more than max_new."""
-        if rows != self.slots.numel():  # kept from step to step while the size stays
-            self.slots = torch.empty(rows, dtype=torch.int32, device=self.lengths.device)
-            self.positions = torch.empty_like(self.slots)
+        if rows != self.slots.numel():
+            if rows not in self._rows:  # kept for good: a captured step holds their addresses
+                self._rows[rows] = tuple(_empty((rows,), torch.int32, self.lengths.device, stream)
+                                         for _ in range(2))
+            self.slots, self.positions = self._rows[rows]
         self.max_new = rows if max_new is None else max_new
         kivi_paged_assign(self.lengths, new_tokens, self.block_table, self.free_pages,
                           self.num_free, self.page_size, kv_lengths=self.lengths,

@@ -79,7 +79,7 @@ struct VarlenAttnArgs {
 cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream);
 long varlen_partial_bytes(int D);
 
-// The requests of few rows (paged form only); scale_log2 = scale * log2 e.
+// Calls whose max_new rows fit one tile (paged form only); scale_log2 = scale * log2 e.
 cudaError_t launch_paged_decode(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream);
 long paged_decode_partial_bytes(int D);
 

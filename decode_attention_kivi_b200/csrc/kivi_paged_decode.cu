@@ -107,7 +107,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       bool bad = false;
       const Request r = load_request(a, b, &bad);
       if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
-      if (r.n > 0 && is_short(r.n, hpk)) v = (long long)a.Hkv * tiles_of(r);
+      if (r.n > 0) v = (long long)a.Hkv * tiles_of(r);  // at most max_new rows, which fit the tile
     }
     long long inc = v;
 #pragma unroll
@@ -518,6 +518,7 @@ cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t str
 long paged_decode_partial_bytes(int D) { return (long)kMaxGrid * 2 * kDecodeRows * (D + 2) * 4; }
 
 cudaError_t launch_paged_decode(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream) {
+  if (!is_short(a.max_new, a.Hq / a.Hkv)) return cudaErrorInvalidValue;
   if (a.dtype == 0)
     return a.D == 128 ? launch_t<__nv_bfloat16, 128>(a, scale_log2, stream)
                       : launch_t<__nv_bfloat16, 64>(a, scale_log2, stream);

@@ -11,8 +11,8 @@
 
 namespace kivi {
 
-// Requests whose n * (query heads per kv head) rows fit one 16-row tensor tile are taken by the
-// decode kernel, the others by the chunk kernel.
+// n tokens of a request, n * (query heads per kv head) rows, that fit the decode kernel's 16-row
+// tensor tile.
 constexpr int kDecodeRows = 16;
 __host__ __device__ __forceinline__ bool is_short(int n, int hpk) { return n <= kDecodeRows / hpk; }
 

@@ -129,12 +129,17 @@ __device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, co
   return kmax < 0 ? 1 : kmax / kTileV + 1;
 }
 
-// Work of a tile of the item (both halves' units, or the one half's), and of an item.
+// Work of a tile of the item, and of an item.  Both halves' units, or the one half's; over pages a
+// lone half's tile counts as three: it waits for its copies as long as both would (the step of the
+// launcher's comment takes 135 us at two, 118 at three, 131 at four; prompts of their own keys, which
+// few of the halves are alone in, take 125 us at two and 131 at three).
+template <bool PAGED>
 __device__ __forceinline__ int tile_work(int rows, int row0) {
-  return rows - row0 > kHalf ? 2 * kUnits : kUnits;
+  return rows - row0 > kHalf ? 2 * kUnits : kUnits + (PAGED ? 1 : 0);
 }
+template <bool PAGED>
 __device__ __forceinline__ int item_work(const Request& r, int rows, int tt, const Heads& h) {
-  return kItemCost + item_tiles(r, rows, tt, h) * tile_work(rows, tt * 2 * kHalf);
+  return kItemCost + item_tiles(r, rows, tt, h) * tile_work<PAGED>(rows, tt * 2 * kHalf);
 }
 
 struct Ranges {
@@ -240,7 +245,7 @@ template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreadsV, 1)
 varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, VarlenAttnArgs a, float scale_log2,
-                        bool skip_short, bool join_here) {
+                        bool join_here) {
   using C = VCfg<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -300,19 +305,18 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       bool bad = false;
       r = load_request(a, b, &bad);
       if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
-      if (skip_short && is_short(r.n, hpk)) r.n = 0;
     }
     const int rows = r.n * hpk, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
     long long v = 0;
     if (items <= 4)
-      for (int tt = 0; tt < items; ++tt) v += item_work(r, rows, tt, heads);
+      for (int tt = 0; tt < items; ++tt) v += item_work<PAGED>(r, rows, tt, heads);
     // requests of many items: the warp's lanes share them
     for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
       const int from = __ffs(left) - 1;
       const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
       const int rrows = rr.n * hpk;
       long long sum = 0;
-      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_work(rr, rrows, tt, heads);
+      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_work<PAGED>(rr, rrows, tt, heads);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == from) v = sum;
@@ -373,7 +377,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     const int kvh = (t_begin - prefix[b]) / per_head;
     int x = t_begin - prefix[b] - kvh * per_head;  // work to pass within the head
     for (int i0 = 0; i0 < items; i0 += kThreadsV) {
-      const int tt = i0 + threadIdx.x, v = tt < items ? item_work(r, rows, tt, heads) : 0;
+      const int tt = i0 + threadIdx.x, v = tt < items ? item_work<PAGED>(r, rows, tt, heads) : 0;
       int inc = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -635,7 +639,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
           ok = k < kPieces || wait(&piece_empty[k % kPieces], (uint32_t)(k / kPieces - 1) & 1u);
           if (!ok) break;
           // tile j belongs to the CTA whose range holds the end of its work
-          const int w = tile_work(r.n * hpk, p.row0);
+          const int w = tile_work<PAGED>(r.n * hpk, p.row0);
           const bool more = t0 + w <= t_end;
           p.j1 = -1;
           if (more) {
@@ -823,8 +827,7 @@ varlen_join_kernel(VarlenAttnArgs a) {
 }
 
 template <typename T, int D, bool PAGED>
-cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, bool skip_short,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream) {
   using C = VCfg<D>;
   int unused = 0;
   cudaError_t e = per_device_setup(a.device, &unused, [](int* v) {
@@ -851,19 +854,18 @@ cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, bool skip_short,
   const int grid = a.num_sms < kMaxGrid ? a.num_sms : kMaxGrid;
   const bool join_here = (long)a.T * a.Hq >= 4L * 2 * kHalf * grid;
   e = launch_pdl(varlen_attention_kernel<T, D, PAGED>, dim3(grid), dim3(kThreadsV), C::bytes(a.B),
-                 stream, tk, tv, a, scale_log2, skip_short, join_here);
+                 stream, tk, tv, a, scale_log2, join_here);
   if (e != cudaSuccess || join_here) return e;
   return launch_pdl(varlen_join_kernel<T, D>, dim3(grid * kSoftWarpsV), dim3(256), 0, stream, a);
 }
 
 template <typename T>
-cudaError_t launch_form(const VarlenAttnArgs& a, float scale_log2, bool skip_short,
-                        cudaStream_t stream) {
+cudaError_t launch_form(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream) {
   if (a.table == nullptr)
-    return a.D == 128 ? launch_t<T, 128, false>(a, scale_log2, skip_short, stream)
-                      : launch_t<T, 64, false>(a, scale_log2, skip_short, stream);
-  return a.D == 128 ? launch_t<T, 128, true>(a, scale_log2, skip_short, stream)
-                    : launch_t<T, 64, true>(a, scale_log2, skip_short, stream);
+    return a.D == 128 ? launch_t<T, 128, false>(a, scale_log2, stream)
+                      : launch_t<T, 64, false>(a, scale_log2, stream);
+  return a.D == 128 ? launch_t<T, 128, true>(a, scale_log2, stream)
+                    : launch_t<T, 64, true>(a, scale_log2, stream);
 }
 
 }  // namespace
@@ -877,13 +879,13 @@ long varlen_partial_bytes(int D) {
 
 cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream) {
   const float scale = (a.sm_scale > 0.f ? a.sm_scale : 1.f / std::sqrt((float)a.D)) * kLog2eV;
-  const bool decode = a.table != nullptr && is_short(1, a.Hq / a.Hkv);
-  if (decode) {
-    const cudaError_t e = launch_paged_decode(a, scale, stream);
-    if (e != cudaSuccess || is_short(a.max_new, a.Hq / a.Hkv)) return e;
-  }
-  return a.dtype == 0 ? launch_form<__nv_bfloat16>(a, scale, decode, stream)
-                      : launch_form<__half>(a, scale, decode, stream);
+  // Single tokens go to the decode kernel.  Where some request may have more rows than its tile,
+  // all of them come here: 30 decoding requests beside two chunks of 509 rows, contexts of 4K, take
+  // 118 us in one launch and 137 us as the decode kernel and this one in turn.
+  if (a.table != nullptr && is_short(a.max_new, a.Hq / a.Hkv))
+    return launch_paged_decode(a, scale, stream);
+  return a.dtype == 0 ? launch_form<__nv_bfloat16>(a, scale, stream)
+                      : launch_form<__half>(a, scale, stream);
 }
 
 }  // namespace kivi

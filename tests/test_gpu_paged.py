@@ -375,6 +375,88 @@ def test_bad_device_values_are_reported(kivi):
     assert (out[:41] == -5.0).all() and not (out[41] == -5.0).any()
 
 
+@pytest.mark.parametrize("hkv,ratio,dim,dtype", [(8, 1, 128, BF16), (4, 4, 64, FP16),
+                                                 (2, 16, 128, BF16)])
+def test_packed_items_cut_and_whole(kivi, hkv, ratio, dim, dtype):
+    """Enough rows that cut items are joined by their last CTA (four items of 256 rows per SM)."""
+    rows = 4 * 256 * 160 // (hkv * ratio)
+    first = rows // 3
+    check_packed(kivi, [first, 1, rows - first - 130, 0, 129], hkv, ratio, dim, dtype, calls=2)
+
+
+def test_chunk_many_requests(kivi):
+    check_paged(kivi, [(b % 90, b % 4) for b in range(4096)], 1, 8, 64, 16)
+
+
+def test_growing_scores(kivi):
+    """Row maxima that grow by more than the rescaling slack from tile to tile, and fall again."""
+    gen = gen_of(21)
+    for n, chunk, dtype in ((700, 700, BF16), (700, 90, FP16), (900, 1, BF16)):
+        K, hkv, hq, dim = kivi, 2, 4, 64
+        pool = Pool(gen, [n], hkv, dim, 32, dtype)
+        # keys along one direction whose length changes: scores up to 60, in steps of 64 keys
+        size = torch.tensor([0.1, 2.0, 0.5, 4.0, 1.0, 6.0, 7.5, 0.2], device="cuda")
+        scale = size[(torch.arange(n, device="cuda") // 64) % 8]
+        base = torch.ones(dim, device="cuda")
+        keys = (scale[:, None, None] * base + 0.05 * torch.randn(n, hkv, dim, generator=gen,
+                                                                 device="cuda")).to(dtype)
+        pool.keys[0] = keys
+        j = torch.arange(n, device="cuda")
+        ids = pool.table[0].long()[j // 32]
+        pool.k[ids, :, j % 32] = keys
+        q = (1.0 + 0.05 * torch.randn(chunk, hq, dim, generator=gen, device="cuda")).to(dtype)
+        got = K.kivi_paged_attention(q, pool.k, pool.v, pool.table, ints([n]), ints([0, chunk]),
+                                     workspace(K, hkv, hq, dim), max_new=chunk)
+        out, mean = U.attend(q, keys, pool.values[0])
+        # scores reach 60: sum |q k| / sqrt(D) is 60 here, 4 times the bound of paged_util's
+        # derivation, so the part of the scores' roundings grows by 4
+        u = torch.finfo(dtype).eps / 2
+        err = (got.double() - out).abs()
+        assert (err <= (3 * u + 4 * 2.0 ** -11) * mean + 1e-6).all(), err.max().item()
+
+
+def test_far_pages(kivi):
+    """A pool of more than 2^31 elements, the requests' pages at its end and a prefix page shared."""
+    gen = gen_of(31)
+    hkv, hq, dim, page = 8, 16, 128, 64
+    pages = (2 ** 31 // (hkv * dim * page)) + 40
+    kp, vp = (torch.zeros(pages, hkv, page, dim, dtype=BF16, device="cuda") for _ in range(2))
+    table = ints([[pages - 1, 3, pages - 2], [pages - 1, pages - 3, 5]])
+    lengths, new = [150, 130], [1, 40]
+    keys, values = ([randn(gen, n, hkv, dim) for n in lengths] for _ in range(2))
+    keys[1][:64], values[1][:64] = keys[0][:64], values[0][:64]
+    slots = torch.cat([table[b].long()[torch.arange(n, device="cuda") // page] * page
+                       + torch.arange(n, device="cuda") % page
+                       for b, n in enumerate(lengths)]).to(torch.int32)
+    slots[lengths[0]:lengths[0] + 64] = -1  # the shared page is written once
+    kivi.kivi_paged_append(torch.cat(keys), torch.cat(values), slots, kp, vp)
+    ws = workspace(kivi, hkv, hq, dim)
+    for new in ([1, 1], [1, 40]):
+        q = randn(gen, sum(new), hq, dim)
+        off = offsets_of(new)
+        got = kivi.kivi_paged_attention(q, kp, vp, table, ints(lengths), ints(off), ws,
+                                        max_new=max(new))
+        for b in range(2):
+            at = slice(off[b], off[b + 1])
+            U.assert_close(got[at], *U.attend(q[at], keys[b], values[b]), f"request {b} of {new}")
+    assert kivi.kivi_attention_status(ws) == 0
+
+
+def test_more_tiles_than_a_call_counts(kivi):
+    """Lengths whose tiles an int does not hold: refused on the device before any copy."""
+    hkv, page, width = 128, 256, 2 ** 23 - 2
+    kp = torch.zeros(1, hkv, page, 64, dtype=BF16, device="cuda")
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    ws = workspace(kivi, hkv, hkv, 64)
+    for n in (1, 300):
+        q = torch.zeros(n, hkv, 64, dtype=BF16, device="cuda")
+        out = torch.full_like(q, -5.0)
+        kivi.kivi_paged_attention(q, kp, kp, table, ints([page * width]), ints([0, n]), ws,
+                                  max_new=n, out=out)
+        assert kivi.kivi_attention_status(ws) == 4
+        assert (out == -5.0).all()
+
+
 # ---- together ----
 
 def run_steps(K, prompts, chunk, decode, hkv, hq, dim, page, dtype, layers=2, seed=1):
@@ -526,3 +608,77 @@ def test_binding_checks(kivi):
             bad()
     with pytest.raises(kivi.KiviError, match="BUFFER_TOO_SMALL"):
         kivi.kivi_packed_attention(q, k, k, off, ws[:128])
+
+
+def test_mixed_steps_in_two_graphs(kivi):
+    """Two captured steps with a workspace each, replayed in turn and with an eager step between,
+    against the plain form: cut items, joined by the second kernel."""
+    gen = gen_of(17)
+    lengths, new = [2100, 333, 64, 900], [1, 120, 64, 30]
+    off, total = offsets_of(new), sum(new)
+    states = []
+    for i in range(2):
+        pool = Pool(gen, lengths, 2, 128, 32, BF16)
+        q = randn(gen, total, 8, 128)
+        out = torch.zeros_like(q)
+        states.append((pool, q, out, workspace(kivi, 2, 8, 128), ints(lengths), ints(off)))
+
+    def call(st, out):
+        pool, q, _, ws, kv, offsets = st
+        return kivi.kivi_paged_attention(q, pool.k, pool.v, pool.table, kv, offsets, ws,
+                                         max_new=max(new), out=out)
+
+    graphs = []
+    for st in states:
+        call(st, None)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(st, st[2])
+        graphs.append(graph)
+    for _ in range(3):
+        for st, graph in zip(states, graphs):
+            st[1].copy_(randn(gen, total, 8, 128))
+            st[2].fill_(-1.0)
+            graph.replay()
+            eager = call(st, None)
+            assert torch.equal(eager, st[2])
+            for b, (a, e) in enumerate(zip(off, off[1:])):
+                U.assert_close(st[2][a:e], *U.attend(st[1][a:e], st[0].keys[b], st[0].values[b]),
+                               f"request {b}")
+    assert all(kivi.kivi_attention_status(st[3]) == 0 for st in states)
+
+
+def test_cache_steps_of_changing_size_keep_a_captured_step(kivi):
+    """A captured decode step of a PagedCache stays valid when an eager step has another size."""
+    gen = gen_of(19)
+    cache, q, k, v = graph_state(kivi, gen)
+    first, keys, values = [5, 14, 31], [], []
+    kk, vv = randn(gen, sum(first), 2, 128), randn(gen, sum(first), 2, 128)
+    cache.assign(ints(first), sum(first))
+    cache.append(0, kk, vv)
+    for a, e in zip(offsets_of(first), offsets_of(first)[1:]):
+        keys.append(kk[a:e])
+        values.append(vv[a:e])
+    one, out = ints([1, 1, 1]), torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.assign(one, 3, max_new=1)
+        cache.append(0, k, v)
+        cache.attend(0, q, out=out)
+
+    def replay():
+        for x, n in ((q, 8), (k, 2), (v, 2)):
+            x.copy_(randn(gen, 3, n, 128))
+        graph.replay()
+        for b in range(3):
+            keys[b] = torch.cat([keys[b], k[b:b + 1]])
+            values[b] = torch.cat([values[b], v[b:b + 1]])
+            U.assert_close(out[b:b + 1], *U.attend(q[b:b + 1], keys[b], values[b]), f"request {b}")
+
+    replay()
+    kk, vv = randn(gen, 70, 2, 128), randn(gen, 70, 2, 128)
+    cache.assign(ints([0, 70, 0]), 70)
+    cache.append(0, kk, vv)
+    keys[1], values[1] = torch.cat([keys[1], kk]), torch.cat([values[1], vv])
+    replay()
+    assert cache.check_device_status() == 0
