@@ -855,7 +855,9 @@ cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t str
   const bool join_here = (long)a.T * a.Hq >= 4L * 2 * kHalf * grid;
   e = launch_pdl(varlen_attention_kernel<T, D, PAGED>, dim3(grid), dim3(kThreadsV), C::bytes(a.B),
                  stream, tk, tv, a, scale_log2, join_here);
-  if (e != cudaSuccess || join_here) return e;
+  // items of one tile are never cut
+  const long keys = PAGED ? (long)a.width << a.page_shift : a.T;
+  if (e != cudaSuccess || join_here || keys <= kTileV) return e;
   return launch_pdl(varlen_join_kernel<T, D>, dim3(grid * kSoftWarpsV), dim3(256), 0, stream, a);
 }
 
