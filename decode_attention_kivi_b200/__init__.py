@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from ._native import KiviBuffers, KiviConfig, KiviError, KiviSizes, check, lib
+from ._native import KiviBuffers, KiviConfig, KiviError, KiviSizes, binding, check, lib
 
 __all__ = [
     "KiviCache", "KiviConfig", "KiviError", "make_config",
@@ -287,36 +287,9 @@ class Bf16Attention:
 
 # ---- the paged 16-bit cache and attention over packed rows ----
 
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # KIVI_BF16, KIVI_FP16
-
-
-def _one_device(*tensors) -> int:
-    """All tensors on one CUDA device, the current one (whose stream the call takes): its index."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device is needed")
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
-    return dev
-
-
-def _stream_on(dev: int, stream) -> int:
-    """The raw stream of a call; the current one is asked for without a Stream object around it,
-    which takes as long as a launch."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between rows of t [rows][heads][channels]: a row is contiguous, rows may be apart
-    (a slice of a wider projection)."""
-    _, heads, dim = t.shape
-    row, head, chan = t.stride()
-    if (chan != 1 and dim > 1) or (head != dim and heads > 1):
-        raise ValueError(f"{name}: heads and channels of a row must be contiguous")
-    return heads * dim if t.shape[0] < 2 else row
+def _raw_stream(stream) -> int | None:
+    """None for the current stream, which the binding asks for itself."""
+    return None if stream is None else _stream(stream)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -327,23 +300,6 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _int_array(t: torch.Tensor, shape, name: str) -> int:
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return t.data_ptr()
-
-
-def _pages(k_pages, v_pages, dtype=None):
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
-        raise ValueError("pages: k and v [num_pages][Hkv][page_size][D]")
-    if k_pages.dtype not in _DTYPES or v_pages.dtype != k_pages.dtype \
-            or (dtype is not None and k_pages.dtype != dtype):
-        raise ValueError(f"pages must be bf16 or fp16 like the rows, got {k_pages.dtype}")
-    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
-        raise ValueError("pages must be contiguous")
-    return k_pages.shape
 
 
 def kivi_attention_workspace_bytes(num_kv_heads: int, num_q_heads: int, head_dim: int) -> int:
@@ -357,8 +313,9 @@ def kivi_attention_workspace_bytes(num_kv_heads: int, num_q_heads: int, head_dim
 def kivi_attention_status(workspace: torch.Tensor, stream=None) -> int:
     """Reads and clears the status word of an attention workspace (0: nothing reported)."""
     code = ctypes.c_uint32()
-    dev = _one_device(workspace)
-    rc = lib().kivi_attention_status(_ptr(workspace, name="workspace"), _stream_on(dev, stream),
+    if workspace.get_device() != torch.cuda.current_device():
+        raise ValueError(f"workspace on {workspace.device}: the current device is needed")
+    rc = lib().kivi_attention_status(_ptr(workspace, name="workspace"), _stream(stream),
                                      ctypes.byref(code))
     if rc not in (0, 7):
         check(rc, "kivi_attention_status")
@@ -374,20 +331,9 @@ def kivi_paged_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_tab
     block_table [B][W] from the stack free_pages / num_free by what new_tokens [B] need beyond
     lengths [B], and fills kv_lengths [B], num_free_out [1], offsets [B+1], slots and positions
     [rows].  Negative new_tokens release a request.  All int32; `status` [1] collects failures."""
-    dev = _one_device(lengths, new_tokens, block_table, free_pages, num_free, kv_lengths, num_free_out,
-                offsets, slots, positions, status)
-    if block_table.dim() != 2 or free_pages.dim() != 1 or slots.dim() != 1:
-        raise ValueError("block_table [B][W], free_pages [num_pages], slots [rows]")
-    B, width = block_table.shape
-    pages, rows = free_pages.shape[0], slots.shape[0]
-    check(lib().kivi_paged_assign(
-        _int_array(lengths, (B,), "lengths"), _int_array(new_tokens, (B,), "new_tokens"), B,
-        _int_array(block_table, (B, width), "block_table"), width,
-        _int_array(free_pages, (pages,), "free_pages"), _int_array(num_free, (1,), "num_free"),
-        pages, page_size, _int_array(kv_lengths, (B,), "kv_lengths"),
-        _int_array(num_free_out, (1,), "num_free_out"), _int_array(offsets, (B + 1,), "offsets"),
-        _int_array(slots, (rows,), "slots"), _int_array(positions, (rows,), "positions"), rows,
-        _int_array(status, (1,), "status"), _stream_on(dev, stream)), "kivi_paged_assign")
+    check(binding().assign(lengths, new_tokens, block_table, free_pages, num_free, page_size,
+                           kv_lengths, num_free_out, offsets, slots, positions, status,
+                           _raw_stream(stream)), "kivi_paged_assign")
 
 
 def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
@@ -395,17 +341,8 @@ def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Ten
                       status: torch.Tensor | None = None, stream=None) -> None:
     """Writes k_new, v_new [rows][Hkv][D] into the slots [rows] of one layer's pages
     [num_pages][Hkv][page_size][D] (bf16 or fp16); rows with a negative slot are skipped."""
-    dev = _one_device(k_new, v_new, slots, k_pages, v_pages, status)
-    pages, hkv, page, dim = _pages(k_pages, v_pages, k_new.dtype)
-    rows = k_new.shape[0]
-    if k_new.shape != (rows, hkv, dim) or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
-        raise ValueError("k_new and v_new must be [rows][Hkv][D] of the pages' type")
-    check(lib().kivi_paged_append(
-        k_new.data_ptr(), _row_stride(k_new, "k_new"), v_new.data_ptr(),
-        _row_stride(v_new, "v_new"), _int_array(slots, (rows,), "slots"), rows,
-        k_pages.data_ptr(), v_pages.data_ptr(), pages, page, hkv, dim,
-        None if status is None else _int_array(status, (1,), "status"), _stream_on(dev, stream)),
-        "kivi_paged_append")
+    check(binding().append(k_new, v_new, slots, k_pages, v_pages, status, _raw_stream(stream)),
+          "kivi_paged_append")
 
 
 def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -415,23 +352,12 @@ def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Causal attention of packed prompts: q [rows][Hq][D], k and v [rows][Hkv][D] (bf16 or fp16),
     request b in rows offsets[b] .. offsets[b+1]-1 (int32, on the device) -> out like q.  Rows
     behind the last request are left as they were."""
-    dev = _one_device(q, k, v, offsets, workspace, out)
-    if out is None:
+    if stream is not None and out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
-    rows, hq, dim = q.shape
-    hkv = k.shape[1]
-    if k.shape != (rows, hkv, dim) or v.shape != k.shape or out.shape != q.shape:
-        raise ValueError("shapes: q and out [rows][Hq][D], k and v [rows][Hkv][D]")
-    if q.dtype not in _DTYPES or not (q.dtype == k.dtype == v.dtype == out.dtype):
-        raise ValueError(f"q, k, v and out must all be bf16 or all fp16, got {q.dtype}")
-    B = offsets.numel() - 1
-    check(lib().kivi_packed_attention(
-        q.data_ptr(), _row_stride(q, "q"), k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
-        _row_stride(v, "v"), out.data_ptr(), _row_stride(out, "out"), _DTYPES[q.dtype],
-        _int_array(offsets, (B + 1,), "offsets"), B, rows, hkv, hq, dim, float(sm_scale),
-        _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
-        _stream_on(dev, stream)), "kivi_packed_attention")
-    return out
+    got = binding().packed(q, k, v, offsets, workspace, out, sm_scale, _raw_stream(stream))
+    if type(got) is int:
+        check(got, "kivi_packed_attention")
+    return got
 
 
 def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -443,23 +369,13 @@ def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     offsets[b+1]-1) over its kv_lengths[b] keys in the pages of block_table[b], causal, the new
     tokens being the last keys -> out like q.  max_new: no request has more new rows (1 in a
     decode step; by default the number of rows)."""
-    dev = _one_device(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, out)
-    if out is None:
+    if stream is not None and out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
-    rows, hq, dim = q.shape
-    pages, hkv, page, pdim = _pages(k_pages, v_pages, q.dtype)
-    if pdim != dim or out.shape != q.shape or out.dtype != q.dtype or block_table.dim() != 2:
-        raise ValueError("shapes: q and out [rows][Hq][D], pages [num_pages][Hkv][page_size][D]")
-    B, width = block_table.shape
-    check(lib().kivi_paged_attention(
-        q.data_ptr(), _row_stride(q, "q"), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
-        _row_stride(out, "out"), _DTYPES[q.dtype],
-        _int_array(block_table, (B, width), "block_table"), width,
-        _int_array(kv_lengths, (B,), "kv_lengths"), _int_array(offsets, (B + 1,), "offsets"), B,
-        rows, max(rows, 1) if max_new is None else int(max_new), pages, page, hkv, hq, dim,
-        float(sm_scale), _ptr(workspace, name="workspace"),
-        workspace.numel() * workspace.element_size(), _stream_on(dev, stream)), "kivi_paged_attention")
-    return out
+    got = binding().paged(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, max_new,
+                          out, sm_scale, _raw_stream(stream))
+    if type(got) is int:
+        check(got, "kivi_paged_attention")
+    return got
 
 
 class PackedAttention:

@@ -1,7 +1,10 @@
-"""ctypes declarations of libkivi.so (include/kivi.h).  Argument marshalling only."""
+"""ctypes declarations of libkivi.so (include/kivi.h), and the loader of the binding of its
+paged-cache and packed-attention calls.  Argument marshalling only."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 # KIVI_LIBRARY selects another in-tree build (the debug library in its tests)
@@ -107,3 +110,27 @@ class KiviError(RuntimeError):
 def check(code: int, where: str) -> None:
     if code != 0:
         raise KiviError(code, where)
+
+
+_binding = None
+
+
+def binding():
+    """The native binding of the paged-cache and packed-attention calls (csrc/kivi_torch.cpp),
+    calling the library that lib() loaded; raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kivi_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it with `python -m decode_attention_kivi_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_kivi_torch", path)
+        spec = importlib.util.spec_from_loader("_kivi_torch", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        L = lib()
+        module.library(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "kivi_paged_assign", "kivi_paged_append", "kivi_packed_attention",
+            "kivi_paged_attention")))
+        _binding = module
+    return _binding

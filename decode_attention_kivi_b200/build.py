@@ -1,14 +1,18 @@
-"""Builds libkivi.so (the C ABI of include/kivi.h) in-tree for sm_100a with nvcc."""
+"""Builds libkivi.so (the C ABI of include/kivi.h) in-tree for sm_100a with nvcc, and
+_kivi_torch.so (the tensor checks and calls of the paged-cache binding) with g++."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkivi.so")
+BINDING = os.path.join(PKG, "_kivi_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "kivi_torch.cpp")
 DEBUG_LIB = os.path.join(PKG, "libkivi_debug.so")
 # debug build: short bounded waits (about 1 ms), copy bounds checks, a test hook
 DEBUG_FLAGS = ["-DKIVI_DEBUG_BUILD", "-DKIVI_DEBUG_BOUNDS", "-DKIVI_DEBUG_WAIT_CYCLES=2000000LL"]
@@ -37,8 +41,32 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Builds _kivi_torch.so against the torch that is installed, when stale."""
+    inputs = [BINDING_SOURCE, os.path.join(ROOT, "include", "kivi.h")]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    dirs = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in dirs], BINDING_SOURCE, "-o", tmp,
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Builds libkivi.so (or, with debug=True, libkivi_debug.so) when stale."""
+    """Builds libkivi.so (or, with debug=True, libkivi_debug.so) and the binding when stale."""
+    build_binding(force and not debug, verbose)
     lib = DEBUG_LIB if debug else LIB
     if not force and not stale(lib):
         return lib
