@@ -19,7 +19,7 @@
 // and, for each of its tiles, the units of 64 keys that its halves go through;
 // every CTA forms the prefix sums that this needs from the device arrays.
 //
-// Twelve warps (two idle), one CTA per SM:
+// Twelve warps (one idle), one CTA per SM:
 //   warp 8 (producer)  2D tensor copies of K and V tiles into a ring of four
 //                      slots, page by page (a box of min(page, 128) rows x 64
 //                      channels per lane) or in one piece;
@@ -31,6 +31,8 @@
 //                      softmax of a half has a unit in hand while the tensor
 //                      cores work on the other.  Units and 16-key steps without
 //                      a key that the half sees are left out;
+//   warp 11 (plan)     one lane lists the CTA's pieces of items a few ahead, for
+//                      the other roles to read;
 //   warps 0-7          one row per thread (its TMEM lane): the row of S from
 //                      TMEM, the mask where the unit needs one, the online
 //                      softmax in base 2, P back to TMEM.  O is rescaled only
@@ -46,6 +48,16 @@
 // O_1 behind it.
 // Every wait is bounded; a wait that runs out sets the status word, and what was
 // issued is drained before TMEM is released.
+//
+// What bounds it (16,384 rows, 32 / 8 heads of 128, bf16): 1.82 ms, 1.21 PFLOP/s,
+// in single passes at 1.75 GHz; 2.09 ms back to back, where the card lowers the
+// clock to hold its power.  A unit of both halves takes 1,780 cycles: its products
+// 1,280 (a step of the scores is 48 cycles at N = 64, 6 KB of operands at 128
+// bytes a cycle, where its arithmetic takes 32), its exponentials 1,024.  Whole
+// tiles of scores (N = 128, 64 cycles a step, no second buffer) let the tensor
+// cores wait for the softmax: 2.09 ms in single passes.  Taking a quarter of the
+// exponentials to the fp32 pipe, fetching the next unit's scores early, and one
+// MMA warp for both halves changed nothing or cost time.
 #include <cmath>
 
 #include "kivi_launch.cuh"
@@ -71,8 +83,11 @@ constexpr int kPieceReaders = 3 + kSoftWarpsV;
 constexpr int kSlabV = 128 * 128;      // 128 rows of 64 channels
 constexpr int kSlots = 4;              // K and V tiles in flight
 constexpr uint32_t kTmemColsV = 512;
-constexpr int kMinWorkV = 8;           // half-units per CTA at least
-constexpr int kItemCost = 8;           // half-units that an item's start and end take as long as
+// Half-units per CTA at least (one tile of one item; 4 and 16 took 20% longer on 700 rows of 8
+// prompts), and those that an item's start and end take as long as: 5.7 by a fit over the CTAs of
+// 8111 packed rows of 13 prompts, 32 heads, which take 131 us at 6, 154 at 4, 133 at 8.
+constexpr int kMinWorkV = 8;
+constexpr int kItemCost = 6;
 constexpr int kChunk = 32;             // scores turned into weights at a time
 // log2 growth of a row maximum before O is rescaled: the weights stay below 2^kSlack, far inside
 // what the type and the 32-bit sums hold, and a larger slack costs no accuracy (the roundings are

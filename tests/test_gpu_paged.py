@@ -608,6 +608,25 @@ def test_binding_checks(kivi):
             bad()
     with pytest.raises(kivi.KiviError, match="BUFFER_TOO_SMALL"):
         kivi.kivi_packed_attention(q, k, k, off, ws[:128])
+    pages = k[None, :2].contiguous()  # one page of 2 "tokens": refused by the library
+    table, one = ints([[0]]), ints([6])
+    for bad in (lambda: kivi.kivi_paged_attention(q, pages, pages, table.long(), one, off, ws),
+                lambda: kivi.kivi_paged_attention(q, pages, pages, table[0], one, off, ws),
+                lambda: kivi.kivi_paged_attention(q, pages, pages, table, ints([6, 6]), off, ws),
+                lambda: kivi.kivi_paged_attention(q, pages, pages.float(), table, one, off, ws),
+                lambda: kivi.kivi_paged_attention(q, pages, pages, table, one, off, ws, out=q[:3]),
+                lambda: kivi.kivi_paged_attention(q, pages, pages, table, one, off, ws,
+                                                  max_new=2 ** 31),
+                lambda: kivi.kivi_packed_attention(q[0], k, k, off, ws),
+                lambda: kivi.kivi_packed_attention(q, k, k, off, ws, out=q.transpose(0, 1)),
+                lambda: kivi.kivi_packed_attention(q[..., ::2], k[..., ::2], k[..., ::2], off, ws)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: kivi.kivi_packed_attention(q, None, k, off, ws),
+                lambda: kivi.kivi_packed_attention(q, k, k, off, ws, sm_scale="x"),
+                lambda: kivi.kivi_paged_attention(q, pages, pages, table, one, off, ws, max_new=1.5)):
+        with pytest.raises(TypeError):
+            bad()
 
 
 def test_mixed_steps_in_two_graphs(kivi):

@@ -113,18 +113,27 @@ def test_attention_status_needs_a_workspace(lib):
     assert N.STATUS[lib.kivi_attention_status(None, None, None)] == "KIVI_ERR_INVALID_ARG"
 
 
-def test_binding_refuses_host_tensors_and_wrong_layouts():
+def test_binding_refuses_host_tensors_and_other_objects():
     import decode_attention_kivi_b200 as K
 
     z = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    n, ws = torch.zeros(2, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA"):
-        K.kivi_packed_attention(z, z, z, torch.zeros(2, dtype=torch.int32),
-                                torch.zeros(256, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="contiguous"):
-        K._row_stride(z.transpose(0, 1), "q")
-    assert K._row_stride(torch.zeros(4, 3 * 128)[:, 128:256].view(4, 2, 64), "q") == 384
-    with pytest.raises(ValueError, match="int32"):
-        K._int_array(torch.zeros(3, dtype=torch.int64), (3,), "offsets")
+        K.kivi_packed_attention(z, z, z, n, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        K.kivi_paged_attention(z, z[None], z[None], n[None], n, n, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        K.kivi_paged_append(z, z, n, z[None], z[None])
+    with pytest.raises(ValueError, match="CUDA"):
+        K.kivi_paged_assign(n, n, n[None], n, n, 16, kv_lengths=n, num_free_out=n, offsets=n,
+                            slots=n, positions=n, status=n)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        K.kivi_packed_attention([1.0], z, z, n, ws)
+    with pytest.raises(TypeError, match="block_table must be a tensor"):
+        K.kivi_paged_assign(n, n, None, n, n, 16, kv_lengths=n, num_free_out=n, offsets=n,
+                            slots=n, positions=n, status=n)
+    with pytest.raises(TypeError, match="arguments"):
+        N.binding().append(z, z)
 
 
 # ---- the plain forms ----
