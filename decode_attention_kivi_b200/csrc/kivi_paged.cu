@@ -15,8 +15,8 @@
 // between the reads of the lengths and the writes of the new lengths, which may
 // be the same array.  A cluster is too few threads for the rows of a large step:
 // above kRowsHere rows a second kernel fills slots and positions from the new
-// tables, four rows per thread (65,000 rows of 500 requests: 24.5 us by the
-// cluster alone, of which the rows took 19).
+// tables, four rows per thread (65,000 rows of 500 requests: 10.5 us, 24.5 by the
+// cluster alone).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -213,6 +213,7 @@ paged_rows_kernel(PagedAssignArgs a) {
 
 // ---- append ----
 
+// Bound by HBM: 16,000 rows of 8 heads of 128, 131 MB read and written, in 24.5 us (5.4 TB/s).
 // One 16-byte vector of K and V per thread and step; a token's row of Hkv * D
 // values is contiguous in the input and one run of D values per head in its page.
 __global__ void __launch_bounds__(256)

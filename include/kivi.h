@@ -400,7 +400,8 @@ kivi_status kivi_fake_quant_keys(const void* k, int64_t rows, int32_t head_dim, 
  *   2  a page id or slot outside the pool (its keys and values read as zeros; the
  *      slot is not written)
  *   4  offsets or lengths outside their buffers or decreasing, a request with
- *      more new tokens than keys or than max_new
+ *      more new tokens than keys or than max_new; lengths whose (row, key) tiles
+ *      in all do not fit 31 bits (the attention computes nothing)
  *   8  not enough free pages */
 #define KIVI_BF16 0
 #define KIVI_FP16 1
@@ -447,7 +448,7 @@ kivi_status kivi_paged_append(const void* k_new, int64_t k_stride, const void* v
                               int32_t num_kv_heads, int32_t head_dim, uint32_t* status,
                               void* stream);
 
-/* Workspace bytes of the two attention calls below: a header of 1 KB (the status
+/* Workspace bytes of the two attention calls below: a header of 8 KB (the status
  * word first) and the partial results of rows whose keys are split.  Host only.
  * The header must be zero-filled before first use and is zero again after each
  * call, except for the status word; calls that share a workspace
@@ -464,6 +465,7 @@ kivi_status kivi_attention_workspace_bytes(int32_t num_kv_heads, int32_t num_q_h
  *   q, out: [rows][num_q_heads][head_dim]; k, v: [rows][num_kv_heads][head_dim].
  *   sm_scale <= 0 means 1/sqrt(head_dim).
  * Inputs of a request must be finite; rows of no request may hold anything.
+ * `out` must not overlap the inputs.  rows * num_q_heads < 2^31 - 512.
  * Errors: INVALID_ARG, UNSUPPORTED, BUFFER_TOO_SMALL (workspace), CUDA. */
 kivi_status kivi_packed_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                   const void* v, int64_t v_stride, void* out, int64_t out_stride,
