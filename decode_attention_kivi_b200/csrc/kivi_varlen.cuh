@@ -1,5 +1,5 @@
 // kivi_varlen.cuh - what the kernels over packed rows share: the two element
-// types, and boxes of page or packed rows as tensor copies.
+// types, paired fp32 arithmetic, and a few more PTX wrappers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,6 +61,34 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// mbar_wait_bounded, given up early once another role of the block set `abort`.
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
+                                                  const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort != 0 || clock64() - t0 > kWaitBudgetCycles) return false;
+  }
+  return true;
+}
+
+// tma_load_2d for three dimensions.
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// One store of 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store_32_bytes(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 }  // namespace kivi
