@@ -213,7 +213,8 @@ paged_rows_kernel(PagedAssignArgs a) {
 
 // ---- append ----
 
-// Bound by HBM: 16,000 rows of 8 heads of 128, 131 MB read and written, in 24.5 us (5.4 TB/s).
+// Bound by HBM: 16,000 rows of 8 heads of 128, 131 MB read and written, in 23.2 us (5.7 TB/s) by
+// one wave of blocks that fills the SMs; 24.5 us by two, 25.5 by as many as there are vectors.
 // One 16-byte vector of K and V per thread and step; a token's row of Hkv * D
 // values is contiguous in the input and one run of D values per head in its page.
 __global__ void __launch_bounds__(256)
@@ -274,7 +275,7 @@ cudaError_t launch_paged_assign(const PagedAssignArgs& a, cudaStream_t stream) {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   const long total = (long)a.T * a.Hkv * (a.D / 8);
   const long blocks = (total + 255) / 256;
-  return launch_pdl(paged_append_kernel, dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16)),
+  return launch_pdl(paged_append_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)),
                     dim3(256), 0, stream, a);
 }
 

@@ -19,7 +19,7 @@
 // and, for each of its tiles, the units of 64 keys that its halves go through;
 // every CTA forms the prefix sums that this needs from the device arrays.
 //
-// Twelve warps (one idle), one CTA per SM:
+// Twelve warps, one CTA per SM:
 //   warp 8 (producer)  2D tensor copies of K and V tiles into a ring of four
 //                      slots, page by page (a box of min(page, 128) rows x 64
 //                      channels per lane) or in one piece;
@@ -58,7 +58,9 @@
 // 1.76 ms here, but 154 us where units take 131 on 8111 rows of 13 prompts, and
 // 140 us for 121 on a step of 32 requests.  Taking a quarter of the exponentials
 // to the fp32 pipe, fetching the next unit's scores early, warps of their own for
-// the items' ends, and one MMA warp for both halves changed nothing or cost time.
+// the items' ends, and one MMA warp for both halves changed nothing or cost time;
+// so did a lone half's tiles taken in turn by both (the step: 165 us), whose ring
+// then holds too few tiles ahead.
 #include <cmath>
 
 #include "kivi_launch.cuh"
