@@ -219,27 +219,48 @@ __device__ __forceinline__ void weights(const float* s, float scale, float mu,
   sum = add2(t[0], t[1]);
 }
 
-// The rows' joined output from `count` partials, in order; src(w) is a warp's state.
-template <typename T, int D, int C4, typename Src>
+// The rows' joined output from `count` partials, in order, kTogether of them in flight at a time;
+// src(w) is a warp's state.
+template <typename T, int D, int C4, int kTogether, typename Src>
 __device__ __forceinline__ void join_rows(int count, Src src, int lane, int c4_0, bool real, T* dst) {
-  float M = -INFINITY;
-  for (int w = 0; w < count; ++w) M = fmaxf(M, __ldcg(src(w) + 32 * D + lane));
-  float L = 0.f, acc[4 * C4];
+  float M = -INFINITY, L = 0.f, acc[4 * C4];
 #pragma unroll
   for (int i = 0; i < 4 * C4; ++i) acc[i] = 0.f;
-  for (int w = 0; w < count; ++w) {
-    const float* s = src(w);
-    const float mw = __ldcg(s + 32 * D + lane);
-    if (mw == -INFINITY) continue;  // nothing seen there, its O is not written
-    const float f = fast_exp2(mw - M);
-    L += f * __ldcg(s + 32 * (D + 1) + lane);
+  for (int w0 = 0; w0 < count; w0 += kTogether) {
+    float mw[kTogether], lw[kTogether];
+    float4 v[kTogether][C4];
 #pragma unroll
-    for (int c = 0; c < C4; ++c) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (c4_0 + c) * 32 + lane);
-      acc[4 * c] += f * v.x;
-      acc[4 * c + 1] += f * v.y;
-      acc[4 * c + 2] += f * v.z;
-      acc[4 * c + 3] += f * v.w;
+    for (int x = 0; x < kTogether; ++x) {
+      mw[x] = -INFINITY;
+      if (w0 + x >= count) continue;
+      const float* s = src(w0 + x);
+      mw[x] = __ldcg(s + 32 * D + lane);
+      lw[x] = __ldcg(s + 32 * (D + 1) + lane);
+#pragma unroll
+      for (int c = 0; c < C4; ++c)
+        v[x][c] = __ldcg(reinterpret_cast<const float4*>(s) + (c4_0 + c) * 32 + lane);
+    }
+    float mn = M;
+#pragma unroll
+    for (int x = 0; x < kTogether; ++x) mn = fmaxf(mn, mw[x]);
+    if (mn == -INFINITY) continue;
+    const float f0 = fast_exp2(M - mn);
+    M = mn;
+    L *= f0;
+#pragma unroll
+    for (int i = 0; i < 4 * C4; ++i) acc[i] *= f0;
+#pragma unroll
+    for (int x = 0; x < kTogether; ++x) {
+      if (mw[x] == -INFINITY) continue;  // nothing seen there, its O is not written
+      const float f = fast_exp2(mw[x] - mn);
+      L += f * lw[x];
+#pragma unroll
+      for (int c = 0; c < C4; ++c) {
+        acc[4 * c] += f * v[x][c].x;
+        acc[4 * c + 1] += f * v[x][c].y;
+        acc[4 * c + 2] += f * v[x][c].z;
+        acc[4 * c + 3] += f * v[x][c].w;
+      }
     }
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -624,7 +645,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             if (lane == 0) arrived = atomicAdd(ticket, 1);
             if (__shfl_sync(0xffffffffu, arrived, 0) == c1 - c0) {
               __threadfence();
-              join_rows<T, D, D / 4>(
+              join_rows<T, D, D / 4, 1>(
                   c1 - c0 + 1,
                   [&](int x) { return partial_of<D>(a, c0 + x, x == 0 ? 1 : 0) + warp * C::kWarpState; },
                   lane, 0, real, dst);
@@ -838,7 +859,7 @@ varlen_join_kernel(VarlenAttnArgs a) {
   const int row = min(row0 + lane, cut.rows - 1), qi = row / hpk;
   T* dst = static_cast<T*>(a.out) + (cut.q0 + qi) * a.out_stride +
            (long)(cut.kvh * hpk + row - qi * hpk) * D;
-  join_rows<T, D, D / 32>(
+  join_rows<T, D, D / 32, 4>(
       cut.count,
       [&](int x) { return partial_of<D>(a, c + x, x == 0 ? 1 : 0) + w8 * VCfg<D>::kWarpState; },
       lane, warp * (D / 32), row0 + lane < cut.rows, dst);
