@@ -171,8 +171,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     c.j = 0;
     if (++c.kvh == a.Hkv) {
       int b = c.b + 1;
-      while (prefix[b + 1] == prefix[b]) ++b;  // the caller has tiles left
-      enter(c, b);
+      // the caller has tiles left (the bound is for lengths that change during the call)
+      while (b + 1 < a.B && prefix[b + 1] == prefix[b]) ++b;
+      enter(c, min(b, a.B - 1));
       c.kvh = 0;
     }
     return true;

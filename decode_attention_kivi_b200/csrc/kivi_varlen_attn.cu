@@ -31,8 +31,8 @@
 //                      softmax of a half has a unit in hand while the tensor
 //                      cores work on the other.  Units and 16-key steps without
 //                      a key that the half sees are left out;
-//   warp 11 (plan)     one lane lists the CTA's pieces of items a few ahead, for
-//                      the other roles to read;
+//   warp 11 (plan)     finds the CTA's range; one lane lists its pieces of items a
+//                      few ahead, for the other roles to read;
 //   warps 0-7          one row per thread (its TMEM lane): the row of S from
 //                      TMEM, the mask where the unit needs one, the online
 //                      softmax in base 2, P back to TMEM.  O is rescaled only
@@ -174,7 +174,7 @@ struct Ranges {
 struct alignas(16) Piece {
   int b, kvh, row0, rows;  // request, kv head, first row and number of rows of the request's heads
   int q0, n, L;            // the request
-  int t0, w;               // where the item's tiles begin in the call's work, and the work of one
+  int c0, c1;              // the CTAs of the item's first and last tile
   int j0, j1, nt;
   int u;                   // tiles of the pieces before, K and V counted
   int e0, e1, pad;
@@ -274,6 +274,35 @@ __device__ __forceinline__ void join_rows(int count, Src src, int lane, int c4_0
                      Elem<T>::pack(acc[4 * c + 6] * inv, acc[4 * c + 7] * inv));
 }
 
+// The work of a lane's request, for a whole warp: the lanes share the requests of many items.
+template <bool PAGED>
+__device__ __forceinline__ long long request_work(const Request& r, const Heads& h, int lane) {
+  const int rows = r.n * h.n, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
+  long long v = 0;
+  if (items <= 4)
+    for (int tt = 0; tt < items; ++tt) v += item_work<PAGED>(r, rows, tt, h);
+  for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
+    const int from = __ffs(left) - 1;
+    const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
+    const int rrows = rr.n * h.n;
+    long long sum = 0;
+    for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_work<PAGED>(rr, rrows, tt, h);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == from) v = sum;
+  }
+  return v;
+}
+template <typename N>
+__device__ __forceinline__ N warp_inclusive(N v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const N o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
 template <int D>
 __device__ __forceinline__ float* partial_of(const VarlenAttnArgs& a, int cta, int which) {
   return reinterpret_cast<float*>(a.partials + kMaxGrid * sizeof(Cut)) +
@@ -300,8 +329,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   uint64_t* drained = piece_empty + kPieces;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, kvh, tt, t0 of the CTA's first item
-  int* s_sum = s_start + 4;                           // [kThreadsV / 32]
+  int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [kThreadsV / 32]
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Heads heads = heads_of(a.Hq / a.Hkv);
@@ -334,10 +362,10 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   }
   wait_for_predecessor();
 
-  // ---- prefix sums of the requests' tiles ----
+  // ---- prefix sums of the requests' work: up to 32 requests are left to the plan warp ----
   long long base = 0;
   bool fits = true;
-  for (int b0 = 0; b0 < a.B; b0 += kThreadsV) {
+  for (int b0 = 0; a.B > 32 && b0 < a.B; b0 += kThreadsV) {
     const int b = b0 + threadIdx.x;
     Request r{0, 0, 0};
     if (b < a.B) {
@@ -345,28 +373,8 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       r = load_request(a, b, &bad);
       if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
     }
-    const int rows = r.n * hpk, items = (rows + 2 * kHalf - 1) / (2 * kHalf);
-    long long v = 0;
-    if (items <= 4)
-      for (int tt = 0; tt < items; ++tt) v += item_work<PAGED>(r, rows, tt, heads);
-    // requests of many items: the warp's lanes share them
-    for (uint32_t left = __ballot_sync(0xffffffffu, items > 4); left; left &= left - 1) {
-      const int from = __ffs(left) - 1;
-      const Request rr{0, __shfl_sync(0xffffffffu, r.n, from), __shfl_sync(0xffffffffu, r.L, from)};
-      const int rrows = rr.n * hpk;
-      long long sum = 0;
-      for (int tt = lane; tt * 2 * kHalf < rrows; tt += 32) sum += item_work<PAGED>(rr, rrows, tt, heads);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == from) v = sum;
-    }
-    v *= a.Hkv;
-    long long inc = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
-    }
+    const long long v = a.Hkv * request_work<PAGED>(r, heads, lane);
+    const long long inc = warp_inclusive(v, lane);
     // a warp's sum that an int does not hold makes the call's total too large
     fits = fits && inc <= INT32_MAX;
     __syncthreads();
@@ -383,65 +391,11 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
     fits = fits && base <= INT32_MAX;
     if (!fits) break;
   }
-  if (threadIdx.x == 0) {
-    prefix[a.B] = (int)base;
-    if (!fits && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
-  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *s_tmem;
   const int cta = blockIdx.x;
-  Ranges sp{0, 0, 0};
-  int t_begin = 0, t_end = 0;
-  if (fits && base > 0) {
-    sp.n = min((int)gridDim.x, (int)((base + kMinWorkV - 1) / kMinWorkV));
-    sp.q = (int)base / sp.n;
-    sp.rem = (int)base - sp.n * sp.q;
-    if (cta < sp.n) {
-      t_begin = sp.lo(cta);
-      t_end = sp.lo(cta + 1);
-    }
-  }
-  // the request and the item that hold t_begin, found by all threads
-  if (t_begin < t_end) {
-    for (int b = threadIdx.x; b < a.B; b += kThreadsV)
-      if (prefix[b] <= t_begin && t_begin < prefix[b + 1]) s_start[0] = b;
-    __syncthreads();
-    const int b = s_start[0];
-    bool bad;
-    const Request r = load_request(a, b, &bad);
-    const int rows = r.n * hpk, items = (rows - 1) / (2 * kHalf) + 1;
-    const int per_head = (prefix[b + 1] - prefix[b]) / a.Hkv;
-    const int kvh = (t_begin - prefix[b]) / per_head;
-    int x = t_begin - prefix[b] - kvh * per_head;  // work to pass within the head
-    for (int i0 = 0; i0 < items; i0 += kThreadsV) {
-      const int tt = i0 + threadIdx.x, v = tt < items ? item_work<PAGED>(r, rows, tt, heads) : 0;
-      int inc = v;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = inc;
-      __syncthreads();
-      int all = 0;
-#pragma unroll
-      for (int w = 0; w < kThreadsV / 32; ++w) {
-        if (w < warp) inc += s_sum[w];
-        all += s_sum[w];
-      }
-      if (v > 0 && inc - v <= x && x < inc) {
-        s_start[1] = kvh;
-        s_start[2] = tt;
-        s_start[3] = t_begin - (x - (inc - v)) + kItemCost;
-      }
-      if (x < all) break;
-      x -= all;
-    }
-  }
-  __syncthreads();
 
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::kOffPieces);
   auto fail = [&]() {
@@ -619,7 +573,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
           }
         }
       } else {
-        const int c0 = sp.cta_of(p.t0 + p.w - 1), c1 = sp.cta_of(p.t0 + p.nt * p.w - 1);
+        const int c0 = p.c0, c1 = p.c1;
         if (p.j0 == 0) cut = Cut{c1 - c0 + 1, p.q0, p.kvh, p.row0, p.rows, {0, 0, 0}};
         if (p.row0 + warp * 32 < p.rows) {
           // slot 0: the item this CTA begins in the middle of; slot 1: the one it leaves unfinished
@@ -661,19 +615,68 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kPlanWarpV) {
-      // ---- plan: the CTA's pieces, by one lane ----
-      if (lane == 0) {
-        bool ok = true, bad;
-        int k = 0, u = 0, t0 = t_end;
-        Piece p{};
+      // ---- plan: the CTA's range, found by the warp, and its pieces, by one lane ----
+      if (a.B <= 32) {
         Request r{0, 0, 0};
-        if (t_begin < t_end) {
-          p.b = s_start[0];
-          p.kvh = s_start[1];
-          p.row0 = s_start[2] * 2 * kHalf;
-          t0 = s_start[3];
-          r = load_request(a, p.b, &bad);
+        if (lane < a.B) {
+          bool bad = false;
+          r = load_request(a, lane, &bad);
+          if (bad && cta == 0) atomicOr(a.status, kPagedBadLength);
         }
+        const long long v = a.Hkv * request_work<PAGED>(r, heads, lane);
+        const long long inc = warp_inclusive(v, lane);
+        base = __shfl_sync(0xffffffffu, inc, 31);
+        fits = base <= INT32_MAX;
+        if (lane < a.B) prefix[lane] = (int)(inc - v);  // used where the total fits
+      }
+      if (lane == 0) {
+        prefix[a.B] = (int)base;
+        if (!fits && cta == 0) atomicOr(a.status, kPagedBadLength);
+      }
+      __syncwarp();
+      Ranges sp{0, 0, 0};
+      int t_begin = 0, t_end = 0;
+      if (fits && base > 0) {
+        sp.n = min((int)gridDim.x, (int)((base + kMinWorkV - 1) / kMinWorkV));
+        sp.q = (int)base / sp.n;
+        sp.rem = (int)base - sp.n * sp.q;
+        if (cta < sp.n) {
+          t_begin = sp.lo(cta);
+          t_end = sp.lo(cta + 1);
+        }
+      }
+      bool ok = true, bad;
+      int t0 = t_end;
+      Piece p{};
+      Request r{0, 0, 0};
+      if (t_begin < t_end) {
+        int lo = 0, hi = a.B;  // largest b with prefix[b] <= t_begin
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (prefix[mid] <= t_begin) lo = mid;
+          else hi = mid;
+        }
+        r = load_request(a, lo, &bad);
+        const int rows = r.n * hpk, per_head = (prefix[lo + 1] - prefix[lo]) / a.Hkv;
+        p.b = lo;
+        p.kvh = (t_begin - prefix[lo]) / per_head;
+        int x = t_begin - prefix[lo] - p.kvh * per_head;  // work to pass within the head
+        for (int i0 = 0; i0 * 2 * kHalf < rows; i0 += 32) {
+          const int tt = i0 + lane;
+          const int v = tt * 2 * kHalf < rows ? item_work<PAGED>(r, rows, tt, heads) : 0;
+          const int inc = warp_inclusive(v, lane);
+          const uint32_t past = __ballot_sync(0xffffffffu, inc > x);
+          if (past) {
+            const int at = __ffs(past) - 1;
+            p.row0 = (i0 + at) * 2 * kHalf;
+            t0 = t_begin - (x - __shfl_sync(0xffffffffu, inc - v, at)) + kItemCost;
+            break;
+          }
+          x -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+      }
+      if (lane == 0) {
+        int k = 0, u = 0;
         for (;; ++k) {
           ok = k < kPieces || wait(&piece_empty[k % kPieces], (uint32_t)(k / kPieces - 1) & 1u);
           if (!ok) break;
@@ -686,11 +689,11 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             p.q0 = r.q0;
             p.n = r.n;
             p.L = r.L;
-            p.t0 = t0;
-            p.w = w;
             p.nt = item_tiles(r, p.rows, p.row0 / (2 * kHalf), heads);
             p.j0 = max(0, t_begin - t0) / w;
             p.j1 = min(p.nt, (t_end - t0) / w);
+            p.c0 = sp.cta_of(t0 + w - 1);
+            p.c1 = sp.cta_of(t0 + p.nt * w - 1);
             p.u = u;
             p.e0 = min(half_units(r, p.rows, p.row0, heads), kUnits * p.j1);
             p.e1 = min(half_units(r, p.rows, p.row0 + kHalf, heads), kUnits * p.j1);
@@ -707,8 +710,11 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
             if (++p.kvh == a.Hkv) {
               p.kvh = 0;
               ++p.b;
-              while (prefix[p.b + 1] == prefix[p.b]) ++p.b;
-              r = load_request(a, p.b, &bad);
+              while (p.b < a.B && prefix[p.b + 1] == prefix[p.b]) ++p.b;
+              if (p.b < a.B)
+                r = load_request(a, p.b, &bad);
+              else
+                t0 = t_end;  // only where the lengths changed during the call
             }
           }
         }
