@@ -38,7 +38,12 @@ constexpr int kTileD = 64;          // keys per tile
 constexpr int kWarpsD = 4;          // consumer warps, 16 keys of each tile
 constexpr int kThreadsD = (kWarpsD + 1) * 32;
 constexpr int kBoxD = kTileD * 128; // 64 rows of 64 channels, the swizzle span
-constexpr int kMinTilesD = 2;       // tiles per CTA at least
+// Tiles per CTA at least: of an item of t tiles cut into p pieces a CTA works through t / p tiles of
+// some 900 cycles, and the last reads p states, for each of its threads' 4-channel groups some 175
+// cycles each, so p = sqrt(5 t / groups) is best (16,000 keys of 16 heads: 66 us at two tiles, 26 at
+// eight, 25 by this rule); then as many tiles as cut the longest item evenly, since a CTA that ends
+// one item and begins the next has two ends to its work (513 keys: 8.4 us at two tiles, 6.8 at three).
+constexpr int kMinTilesD = 2;
 
 template <int D>
 struct DCfg {
@@ -49,7 +54,7 @@ struct DCfg {
   static constexpr int kState = kDecodeRows * (D + 2);  // O[16][D], m[16], l[16]
   static constexpr int kOffMerge = kStages * kStageBytes;
   static constexpr int kOffBars = kOffMerge + kWarpsD * kState * 4;
-  static constexpr int kOffPrefix = kOffBars + 2 * kStages * 8 + 64;
+  static constexpr int kOffPrefix = kOffBars + 2 * kStages * 8 + 80;
   static constexpr int bytes(int B) { return kOffPrefix + 4 * (B + 1) + 1024; }
   static_assert(bytes(kMaxRequests) <= 227 * 1024, "shared-memory plan");
 };
@@ -87,7 +92,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
   int* s_flag = reinterpret_cast<int*>(empty + C::kStages);  // the ticket's verdict
   volatile int* s_abort = s_flag + 1;
   volatile int* s_issued = s_flag + 2;
-  long long* s_sum = reinterpret_cast<long long*>(s_flag + 4);  // [kWarpsD + 1] sums of the scan
+  long long* s_sum = reinterpret_cast<long long*>(s_flag + 4);  // [kWarpsD + 1] sums of the scan,
+  int* s_most = reinterpret_cast<int*>(s_sum + kWarpsD + 1);    // and the most tiles of a request
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hpk = a.Hq / a.Hkv;
@@ -105,14 +111,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
 
   // ---- prefix sums of the requests' tiles ----
   long long base = 0;
+  int longest = 1;  // tiles of an item
   for (int b0 = 0; b0 < a.B; b0 += kThreadsD) {
     const int b = b0 + threadIdx.x;
     long long v = 0;
+    int tiles = 0;
     if (b < a.B) {
       bool bad = false;
       const Request r = load_request(a, b, &bad);
       if (bad && blockIdx.x == 0) atomicOr(a.status, kPagedBadLength);
-      if (r.n > 0) v = (long long)a.Hkv * tiles_of(r);  // at most max_new rows, which fit the tile
+      if (r.n > 0) tiles = tiles_of(r);  // at most max_new rows, which fit the tensor tile
+      v = (long long)a.Hkv * tiles;
     }
     long long inc = v;
 #pragma unroll
@@ -121,13 +130,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       if (lane >= d) inc += o;
     }
     __syncthreads();
-    if (lane == 31) s_sum[warp] = inc;
+    const int most = __reduce_max_sync(0xffffffffu, tiles);
+    if (lane == 31) {
+      s_sum[warp] = inc;
+      s_most[warp] = most;
+    }
     __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w <= kWarpsD; ++w) {
       if (w < warp) before += s_sum[w];
       all += s_sum[w];
+      longest = max(longest, s_most[w]);
     }
     if (b < a.B) prefix[b] = (int)(base + before + inc - v);  // used where the total fits
     base += all;
@@ -139,7 +153,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     return;
   }
   Split sp;
-  sp.n = min((int)gridDim.x, (int)((base + kMinTilesD - 1) / kMinTilesD));
+  const int groups = (a.max_new * hpk * (D / 4) + kWarpsD * 32 - 1) / (kWarpsD * 32);
+  const int wanted = max(kMinTilesD, (int)ceilf(sqrtf((float)longest * (float)groups * 0.2f)));
+  const int pieces = max(1, longest / wanted), least = (longest + pieces - 1) / pieces;
+  sp.n = min((int)gridDim.x, (int)((base + least - 1) / least));
   if ((int)blockIdx.x >= sp.n) return;
   sp.q = (int)base / sp.n;
   sp.rem = (int)base - sp.n * sp.q;
