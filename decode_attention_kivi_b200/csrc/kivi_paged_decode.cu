@@ -112,8 +112,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
   // ---- prefix sums of the requests' tiles ----
   long long base = 0;
   int longest = 1;  // tiles of an item
+  // up to 32 requests: every warp forms the sums of all of them
+  const bool alone = a.B <= 32;
   for (int b0 = 0; b0 < a.B; b0 += kThreadsD) {
-    const int b = b0 + threadIdx.x;
+    const int b = b0 + (alone ? lane : (int)threadIdx.x);
     long long v = 0;
     int tiles = 0;
     if (b < a.B) {
@@ -129,8 +131,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       const long long o = __shfl_up_sync(0xffffffffu, inc, d);
       if (lane >= d) inc += o;
     }
-    __syncthreads();
     const int most = __reduce_max_sync(0xffffffffu, tiles);
+    if (alone) {
+      if (warp == 0 && b < a.B) prefix[b] = (int)(inc - v);  // used where the total fits
+      base = __shfl_sync(0xffffffffu, inc, 31);
+      longest = max(longest, most);
+      break;
+    }
+    __syncthreads();
     if (lane == 31) {
       s_sum[warp] = inc;
       s_most[warp] = most;
