@@ -23,8 +23,8 @@
 // do not depend on the order of arrival.
 // Every wait is bounded; a wait that runs out sets the status word.
 //
-// 16 requests of up to 8K keys, 32 / 8 heads of 128, pages of 64: 67.5 us, 5.5 TB/s
-// (84% of the measured copy rate); 8 requests to 4K, 32 heads, pages of 16: 59.6 us,
+// 16 requests of up to 8K keys, 32 / 8 heads of 128, pages of 64: 67 to 69 us, 5.4 TB/s
+// (82% of the measured copy rate); 8 requests to 4K, 32 heads, pages of 16: 59.5 us,
 // 4.9 TB/s.  Of some 130,000 cycles 1,800 are the prologue, 6,000 the way to the
 // first tile (lengths, table, copy, each from DRAM), 6,000 the last item's join.
 #include "kivi_launch.cuh"
