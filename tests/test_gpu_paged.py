@@ -415,6 +415,50 @@ def test_growing_scores(kivi):
         assert (err <= (3 * u + 4 * 2.0 ** -11) * mean + 1e-6).all(), err.max().item()
 
 
+@pytest.mark.parametrize("B", [31, 32, 33])
+def test_request_counts_at_a_warp(kivi, B):
+    """Both ways of forming the ranges (one warp, the whole block), requests without rows among them."""
+    check_paged(kivi, [(5 + 61 * b % 400, b % 3 % 2) for b in range(B)], 2, 4, 128, 16, max_new=1)
+    check_paged(kivi, [(5 + 61 * b % 400, (7 * b) % 6) for b in range(B)], 2, 8, 64, 32)
+    check_packed(kivi, [(37 * b) % 150 for b in range(B)], 2, 2, 64)
+
+
+def test_one_long_request_of_many_heads(kivi):
+    check_paged(kivi, [(16000, 1)], 1, 16, 128, 64, max_new=1, calls=2)
+    check_paged(kivi, [(16000, 3)], 1, 16, 128, 64, calls=2)
+
+
+def test_calls_side_by_side(kivi):
+    """Two streams with a workspace each, many calls at once: as one after the other."""
+    gen = gen_of(23)
+    pool = Pool(gen, [2500, 900, 300], 2, 128, 32, BF16)
+    kv, steps = ints([2500, 900, 300]), []
+    for new in ([300, 1, 90], [1, 1, 1]):
+        off = offsets_of(new)
+        q = randn(gen, off[-1], 8, 128)
+        steps.append((q, ints(off), max(new)))
+
+    def call(step, ws, **kw):
+        q, off, max_new = step
+        return kivi.kivi_paged_attention(q, pool.k, pool.v, pool.table, kv, off, ws,
+                                         max_new=max_new, **kw)
+
+    spaces = [workspace(kivi, 2, 8, 128) for _ in range(2)]
+    want = [call(step, spaces[0]) for step in steps]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, (stream, ws) in enumerate(zip(streams, spaces)):
+            for step in steps:
+                got[i].append(call(step, ws, stream=stream))
+    torch.cuda.synchronize()
+    for outs in got:
+        for j, out in enumerate(outs):
+            assert torch.equal(out, want[j % 2])
+    assert all(kivi.kivi_attention_status(ws) == 0 for ws in spaces)
+
+
 def test_far_pages(kivi):
     """A pool of more than 2^31 elements, the requests' pages at its end and a prefix page shared."""
     gen = gen_of(31)
