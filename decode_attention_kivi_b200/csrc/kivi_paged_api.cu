@@ -6,6 +6,7 @@
 
 #include "../../include/kivi.h"
 #include "kivi_paged.h"
+#include "kivi_status.h"
 
 namespace {
 
@@ -223,12 +224,8 @@ kivi_status kivi_paged_attention(const void* q, int64_t q_stride, const void* k_
 
 kivi_status kivi_attention_status(void* workspace, void* stream, uint32_t* code_out) {
   if (!workspace) return KIVI_ERR_INVALID_ARG;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return KIVI_ERR_CUDA;
   uint32_t code = 0;
-  if (cudaMemcpy(&code, workspace, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess)
-    return KIVI_ERR_CUDA;
-  if (code != 0 && cudaMemset(workspace, 0, kivi::kPagedHeader) != cudaSuccess)
+  if (!kivi::take_status(workspace, kivi::kPagedHeader, static_cast<cudaStream_t>(stream), &code))
     return KIVI_ERR_CUDA;
   if (code_out) *code_out = code;
   return code ? KIVI_ERR_DEVICE : KIVI_OK;

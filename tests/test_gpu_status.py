@@ -1,0 +1,61 @@
+"""The status queries on the GPU (needs a B200): what they read and clear runs on the caller's stream
+and is complete on return.
+
+The default stream is kept busy by a kernel that sleeps while the query runs on another stream: a
+query that touches the default stream would come back only when that kernel has ended."""
+import pytest
+import torch
+
+import paged_util as U
+from gpu_util import load_kivi
+from test_gpu_paged import Pool, gen_of, ints, randn, workspace
+
+pytestmark = pytest.mark.gpu
+BUSY_CYCLES = 1_000_000_000  # about half a second
+
+
+@pytest.fixture(scope="module")
+def kivi():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    return load_kivi()
+
+
+def busy_default_stream():
+    """An event behind about half a second of work on the default stream."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY_CYCLES)
+    end = torch.cuda.Event()
+    end.record()
+    return end
+
+
+@pytest.mark.parametrize("new", [[1, 1], [200, 30]])
+def test_attention_status_clears_on_its_stream(kivi, new):
+    """A call that reports a bad page, the query, and at once calls whose items are cut and joined."""
+    gen = gen_of(41)
+    lengths, off = [3000, 700], ints([0, new[0], sum(new)])
+    pool = Pool(gen, lengths, 2, 128, 32, torch.bfloat16)
+    bad = pool.table.clone()
+    bad[0, 1] = -1
+    q, ws, kv = randn(gen, sum(new), 8, 128), workspace(kivi, 2, 8, 128), ints(lengths)
+    outs = [torch.empty_like(q) for _ in range(6)]
+    stream = torch.cuda.Stream()
+
+    def call(table, out):
+        kivi.kivi_paged_attention(q, pool.k, pool.v, table, kv, off, ws, max_new=max(new), out=out,
+                                  stream=stream)
+
+    call(pool.table, outs[0])  # loads the kernels
+    end = busy_default_stream()
+    for out in outs:
+        call(bad, out)
+        assert kivi.kivi_attention_status(ws, stream) == 2
+        call(pool.table, out)
+    assert kivi.kivi_attention_status(ws, stream) == 0
+    assert not end.query(), "the query waited for the default stream"
+    torch.cuda.synchronize()
+    assert ws[64:8192].count_nonzero() == 0
+    for out in outs:
+        for b, (a, e) in enumerate(zip([0, new[0]], [new[0], sum(new)])):
+            U.assert_close(out[a:e], *U.attend(q[a:e], pool.keys[b], pool.values[b]), f"request {b}")
