@@ -14,6 +14,7 @@
 #include "kivi_kernels.h"
 #include "kivi_launch.cuh"
 #include "kivi_layout.cuh"
+#include "kivi_status.h"
 
 struct kivi_cache {
   kivi_config cfg;
@@ -455,17 +456,12 @@ kivi_status kivi_decode_attention(const kivi_cache* cache, int32_t layer, const 
 
 kivi_status kivi_check_device_status(kivi_cache* cache, void* stream, uint32_t* code_out) {
   if (!cache) return KIVI_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(s) != cudaSuccess) return KIVI_ERR_CUDA;
-  uint32_t code = 0;
-  if (cudaMemcpy(&code, cache->bufs.workspace, sizeof code, cudaMemcpyDeviceToHost) !=
-      cudaSuccess)
-    return KIVI_ERR_CUDA;
   // after a failure the tickets may be left counting: clear them with the word
   const size_t clear =
       kivi::kWsHeader +
       kivi::ws_tickets_bytes((long)cache->cfg.batch * cache->cfg.num_kv_heads);
-  if (code != 0 && cudaMemset(cache->bufs.workspace, 0, clear) != cudaSuccess)
+  uint32_t code = 0;
+  if (!kivi::take_status(cache->bufs.workspace, clear, static_cast<cudaStream_t>(stream), &code))
     return KIVI_ERR_CUDA;
   if (code_out) *code_out = code;
   return code ? KIVI_ERR_DEVICE : KIVI_OK;
@@ -541,13 +537,9 @@ kivi_status kivi_bf16_decode_attention(const void* k_cache, const void* v_cache,
 kivi_status kivi_bf16_status(void* workspace, int32_t batch, int32_t num_kv_heads, void* stream,
                              uint32_t* code_out) {
   if (!workspace || batch < 1 || num_kv_heads < 1) return KIVI_ERR_INVALID_ARG;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return KIVI_ERR_CUDA;
   uint32_t code = 0;
-  if (cudaMemcpy(&code, workspace, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess)
-    return KIVI_ERR_CUDA;
-  if (code != 0 &&
-      cudaMemset(workspace, 0, bf16_fixed_bytes(batch, num_kv_heads)) != cudaSuccess)
+  if (!kivi::take_status(workspace, bf16_fixed_bytes(batch, num_kv_heads),
+                         static_cast<cudaStream_t>(stream), &code))
     return KIVI_ERR_CUDA;
   if (code_out) *code_out = code;
   return code ? KIVI_ERR_DEVICE : KIVI_OK;
@@ -712,13 +704,9 @@ extern "C" kivi_status kivi_static_scratch_status(void* stream, uint32_t* code_o
   StaticScratchSlot slot;
   kivi_status st = static_scratch_slot(s, &slot);
   if (st != KIVI_OK) return st;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return KIVI_ERR_CUDA;
   uint32_t code = 0;
-  if (cudaMemcpy(&code, slot.ptr, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess)
-    return KIVI_ERR_CUDA;
   // after a failure the tickets may be left counting: clear the whole array
-  if (code != 0 && cudaMemset(slot.ptr, 0, KIVI_STATIC_SCRATCH_BYTES) != cudaSuccess)
-    return KIVI_ERR_CUDA;
+  if (!kivi::take_status(slot.ptr, KIVI_STATIC_SCRATCH_BYTES, s, &code)) return KIVI_ERR_CUDA;
   if (code_out) *code_out = code;
   return code ? KIVI_ERR_DEVICE : KIVI_OK;
 }

@@ -59,3 +59,39 @@ def test_attention_status_clears_on_its_stream(kivi, new):
     for out in outs:
         for b, (a, e) in enumerate(zip([0, new[0]], [new[0], sum(new)])):
             U.assert_close(out[a:e], *U.attend(q[a:e], pool.keys[b], pool.values[b]), f"request {b}")
+
+
+def small_cache(K):
+    return K.KiviCache(batch=2, num_layers=1, num_kv_heads=2, num_q_heads=4, head_dim=64, bits=2,
+                       max_tokens=300)
+
+
+def query_of(K, which):
+    """A status query, and the buffer whose first word it takes (None: not reachable from here)."""
+    if which == "cache":
+        cache = small_cache(K)
+        return cache.check_device_status, cache.workspace
+    if which == "bf16":
+        attention = K.Bf16Attention(batch=2, num_kv_heads=2, num_q_heads=4, head_dim=64)
+        return attention.check_device_status, attention.workspace
+    return K.kivi_static_scratch_status, None
+
+
+@pytest.mark.parametrize("which", ["cache", "bf16", "static"])
+def test_older_queries_clear_on_their_stream(kivi, which):
+    """The word and a ticket set as a failed call leaves them, the query, and a read at once."""
+    query, words = query_of(kivi, which)
+    stream = torch.cuda.Stream()
+    assert query(stream) == 0
+    end = busy_default_stream()
+    with torch.cuda.stream(stream):
+        for _ in range(4):
+            if words is not None:
+                words[:64].fill_(1)
+            assert query(stream) == (0 if words is None else 0x01010101)
+            if words is not None:
+                left = words[:64].cpu()
+                assert left.count_nonzero() == 0
+        assert query(stream) == 0
+    assert not end.query(), "the query waited for the default stream"
+    torch.cuda.synchronize()
