@@ -193,7 +193,10 @@ kivi_status kivi_cache_create(const kivi_config* cfg, const kivi_buffers* bufs,
   // status word and tickets start at zero (the decode kernel leaves the tickets at zero)
   const size_t clear = kivi::kWsHeader +
                        kivi::ws_tickets_bytes((long)cfg->batch * cfg->num_kv_heads);
-  if (cudaMemset(bufs->workspace, 0, clear) != cudaSuccess) return KIVI_ERR_CUDA;
+  // complete on return: the handle's first call may come on a stream that does not wait for this one
+  if (cudaMemsetAsync(bufs->workspace, 0, clear, nullptr) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess)
+    return KIVI_ERR_CUDA;
   kivi_cache* h = new (std::nothrow) kivi_cache();
   if (!h) return KIVI_ERR_INVALID_ARG;
   h->cfg = *cfg;

@@ -144,7 +144,8 @@ kivi_status kivi_record_layout(const kivi_config* cfg, size_t* record_bytes,
                                int32_t* records_per_seq);
 
 /* Creates a handle over caller-owned buffers; every layer starts empty (S = 0).
- * Zeroes the device status word in `workspace` with a synchronous cudaMemset.
+ * Zeroes the device status word and the tickets in `workspace` on the legacy stream,
+ * and waits for that: they are clear on return, whatever stream is used next.
  * Errors: INVALID_ARG, UNSUPPORTED, BUFFER_TOO_SMALL, CUDA. */
 kivi_status kivi_cache_create(const kivi_config* cfg, const kivi_buffers* bufs,
                               kivi_cache** out);

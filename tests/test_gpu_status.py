@@ -95,3 +95,17 @@ def test_older_queries_clear_on_their_stream(kivi, which):
         assert query(stream) == 0
     assert not end.query(), "the query waited for the default stream"
     torch.cuda.synchronize()
+
+
+def test_a_new_handle_is_clear_on_return(kivi):
+    """No clear of a new handle's workspace is pending behind the default stream's work."""
+    small_cache(kivi).close()
+    stream = torch.cuda.Stream()
+    end = busy_default_stream()
+    with torch.cuda.stream(stream):
+        cache = small_cache(kivi)
+        assert end.query()
+        cache.workspace[:4].fill_(1)
+        assert cache.check_device_status(stream) == 0x01010101
+        assert cache.check_device_status(stream) == 0
+    cache.close()
