@@ -468,7 +468,9 @@ class KiviCache:
         self.records = torch.empty(max(sizes.records_bytes, 16), dtype=torch.uint8, device=dev)
         self.resid_k = torch.empty(sizes.resid_k_bytes, dtype=torch.uint8, device=dev)
         self.resid_v = torch.empty(sizes.resid_v_bytes, dtype=torch.uint8, device=dev)
-        self.workspace = torch.empty(sizes.workspace_bytes, dtype=torch.uint8, device=dev)
+        # cleared on the stream that the block belongs to: work on a tensor that held it before may
+        # be pending there, behind which the library's own clear of the header does not wait
+        self.workspace = torch.zeros(sizes.workspace_bytes, dtype=torch.uint8, device=dev)
         bufs = KiviBuffers(self.records.data_ptr(), self.resid_k.data_ptr(),
                            self.resid_v.data_ptr(), self.workspace.data_ptr(),
                            KiviSizes(self.records.numel(), self.resid_k.numel(),

@@ -109,3 +109,21 @@ def test_a_new_handle_is_clear_on_return(kivi):
         assert cache.check_device_status(stream) == 0x01010101
         assert cache.check_device_status(stream) == 0
     cache.close()
+
+
+def test_a_new_cache_takes_a_block_with_work_pending(kivi):
+    """The workspace's memory held another tensor, whose last write on the stream is still to come."""
+    sample = small_cache(kivi)
+    shapes = [t.numel() for t in (sample.records, sample.resid_k, sample.resid_v, sample.workspace)]
+    sample.close()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        torch.cuda.synchronize()
+        old = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in shapes]
+        torch.cuda._sleep(BUSY_CYCLES // 4)
+        for t in old:
+            t.fill_(1)
+        del old, t
+        cache = small_cache(kivi)
+        assert cache.check_device_status(stream) == 0
+    cache.close()
