@@ -292,13 +292,16 @@ def _raw_stream(stream) -> int | None:
     return None if stream is None else _stream(stream)
 
 
+def _on(stream, device):
+    """A context in which torch works on the stream that a call was given."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)  # of None: nothing
+
+
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """A new tensor that belongs to the stream the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
+    with _on(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -445,10 +448,15 @@ class PagedCache:
                                     sm_scale, stream)
 
     def check_device_status(self, stream=None) -> int:
-        """The step's failures (bits of kivi.h) since the last query; clears them."""
-        code = kivi_attention_status(self.workspace, stream) | int(self.status.item())
-        self.status.zero_()
-        return code
+        """The step's failures (bits of kivi.h) since the last query; clears them.  Waits for
+        `stream`, on which the words are read and cleared; they are clear on return."""
+        code = kivi_attention_status(self.workspace, stream)
+        with _on(stream, self.status.device):
+            step = int(self.status.item())
+            if step:
+                self.status.zero_()
+                torch.cuda.current_stream(self.status.device).synchronize()
+        return code | step
 
 
 def kivi_status_string(code: int) -> str:

@@ -127,3 +127,27 @@ def test_a_new_cache_takes_a_block_with_work_pending(kivi):
         cache = small_cache(kivi)
         assert cache.check_device_status(stream) == 0
     cache.close()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_paged_cache_query_clears_on_its_stream(kivi, raw):
+    """Steps that fail on a stream beside a busy default stream: each query has its own step's bits."""
+    cache = kivi.PagedCache(num_pages=4, page_size=16, num_layers=1, num_kv_heads=1, num_q_heads=2,
+                            head_dim=64, max_requests=2, max_tokens=64)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    fits, pages, long = ints([1, 0]), ints([50, 50]), ints([65, 0])
+    cache.assign(fits, 1)
+    cache.assign(pages, 100)
+    cache.check_device_status()
+    end = busy_default_stream()
+    for _ in range(3):
+        cache.assign(pages, 100, stream=stream)
+        assert cache.check_device_status(stream) == 8
+        cache.assign(long, 100, stream=stream)
+        assert cache.check_device_status(stream) == 4
+        cache.assign(fits, 1, stream=stream)
+        assert cache.check_device_status(stream) == 0
+    assert not end.query(), "the query waited for the default stream"
+    torch.cuda.synchronize()
+    assert cache.lengths.tolist() == [4, 0]
