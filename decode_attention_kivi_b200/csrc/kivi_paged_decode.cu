@@ -44,6 +44,12 @@ constexpr int kBoxD = kTileD * 128; // 64 rows of 64 channels, the swizzle span
 // eight, 25 by this rule); then as many tiles as cut the longest item evenly, since a CTA that ends
 // one item and begins the next has two ends to its work (513 keys: 8.4 us at two tiles, 6.8 at three).
 constexpr int kMinTilesD = 2;
+// log2 of a row's largest weight.  A bf16 weight is rounded relative to itself; a fp16 one has steps
+// of 2^-24 below 2^-14, so that without the factor (which O / l does not see) a long tail of keys near
+// 2^-25 of the row's largest would be lost to P V and still counted in l.  Added behind the
+// subtraction, which is exact for the largest scores whatever their size: no weight exceeds 2^15.
+template <typename T>
+constexpr float kTopD = Elem<T>::kBf16 ? 0.f : 15.f;
 
 template <int D>
 struct DCfg {
@@ -480,7 +486,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         m[e] = mn;
         float w[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) w[y] = fast_exp2(x[y] - mu);
+        for (int y = 0; y < 4; ++y)
+          w[y] = fast_exp2(Elem<T>::kBf16 ? x[y] - mu : (x[y] - mu) + kTopD<T>);
         l[e] = l[e] * al[e] + ((w[0] + w[1]) + (w[2] + w[3]));
         p[e] = Elem<T>::pack(w[0], w[1]);
         p[2 + e] = Elem<T>::pack(w[2], w[3]);

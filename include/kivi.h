@@ -463,7 +463,8 @@ kivi_status kivi_attention_workspace_bytes(int32_t num_kv_heads, int32_t num_q_h
  *   out[t][h] = sum_j softmax_j(sm_scale * <q[t][h], k[j][kvh]>) v[j][kvh]
  * over the rows j of the same request up to t, kvh = h / (num_q_heads /
  * num_kv_heads).  fp32 scores, statistics and accumulation; the softmax weights
- * are rounded to the element type for the second product, the result once.
+ * are rounded to the element type for the second product (fp16: those below 2^-20
+ * of the row's largest to 2^-31 of that), the result once.
  *   q, out: [rows][num_q_heads][head_dim]; k, v: [rows][num_kv_heads][head_dim].
  *   sm_scale <= 0 means 1/sqrt(head_dim).
  * Inputs of a request must be finite; rows of no request may hold anything.

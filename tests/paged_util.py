@@ -9,6 +9,9 @@ Tolerance of an attention output element, from the arithmetic.  With u the type'
     D 2^-24 sum |q k| sm_scale of itself, under 130 * 2^-24 * 16 < 2^-13 for the unit-normal rows
     here (sum |q k| / sqrt(D) stays below 16), and the exponential is within 2^-13 relative, so a
     weight is within 2^-12 and the quotient within 2 * 2^-12 = 2^-11 of A.
+  - a fp16 weight in the type's subnormal range is off by up to 2^-31 of the row's largest, not by u of
+    itself: with L keys up to L 2^-31 max |v|, which the inputs here leave far below the 1e-6 (few
+    keys lie so far below the largest) and test_gpu_paged_tails.py counts.
 So |out - exact| <= (3u + 2^-11) A + 1e-6 (the last for results in the type's subnormal range).
 """
 import math
