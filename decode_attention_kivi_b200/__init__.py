@@ -426,13 +426,14 @@ class PagedCache:
     def assign(self, new_tokens: torch.Tensor, rows: int, max_new: int | None = None,
                stream=None) -> None:
         """Starts a step: new_tokens [max_requests] (int32, device; negative releases), `rows`
-        packed rows in the step's buffers, of which no request has more than max_new."""
+        packed rows in the step's buffers (none where all requests are idle or released), of which no
+        request has more than max_new."""
         if rows != self.slots.numel():
             if rows not in self._rows:  # kept for good: a captured step holds their addresses
                 self._rows[rows] = tuple(_empty((rows,), torch.int32, self.lengths.device, stream)
                                          for _ in range(2))
             self.slots, self.positions = self._rows[rows]
-        self.max_new = rows if max_new is None else max_new
+        self.max_new = max(1, rows if max_new is None else max_new)  # a step may have no row
         kivi_paged_assign(self.lengths, new_tokens, self.block_table, self.free_pages,
                           self.num_free, self.page_size, kv_lengths=self.lengths,
                           num_free_out=self.num_free, offsets=self.offsets, slots=self.slots,

@@ -205,7 +205,7 @@ kivi_status kivi_paged_attention(const void* q, int64_t q_stride, const void* k_
   st = attention_args(a, dtype, q, q_stride, out, out_stride, offsets, batch, rows, num_kv_heads,
                       num_q_heads, head_dim, sm_scale, workspace, workspace_bytes);
   if (st != KIVI_OK) return st;
-  if (max_new < 1 || !tokens_ok(num_pages, page_size) || !tokens_ok(table_width, page_size) ||
+  if (max_new < (rows > 0 ? 1 : 0) || !tokens_ok(num_pages, page_size) || !tokens_ok(table_width, page_size) ||
       (int64_t)num_pages * page_size * num_kv_heads > INT32_MAX || !int_array(block_table) ||
       !int_array(kv_lengths))
     return KIVI_ERR_INVALID_ARG;

@@ -480,8 +480,8 @@ kivi_status kivi_packed_attention(const void* q, int64_t q_stride, const void* k
 /* Attention of each request's new tokens over its pages.  Request b holds
  * kv_lengths[b] keys, the step's among them (appended before this call); its
  * row i of n sees keys 0 .. kv_lengths[b] - n + i.  A row without keys is 0.
- * max_new: no request of the step has more new rows (1 for a decode step); a
- * request that has more is not computed and sets bit 4.  What the pages hold
+ * max_new: no request of the step has more new rows (1 for a decode step; at least 1
+ * where there are rows); a request that has more is not computed and sets bit 4.  What the pages hold
  * behind a request's last key may be anything.  Otherwise as
  * kivi_packed_attention.
  * Errors: INVALID_ARG (also num_pages * page_size * num_kv_heads >= 2^31),

@@ -164,3 +164,10 @@ def test_books_by_hand():
     assert b.step([0, 8, 3], 8)[3] == 4                                 # more rows than there are
     b.num_free = 1
     assert b.step([0, 8, 0], 8) == ([0] * 4, [-1] * 8, [0] * 8, 8)      # not enough pages
+
+
+def test_paged_attention_without_rows_takes_a_max_new_of_zero(lib):
+    """The largest number of new rows of a step that has none."""
+    a = {**PAGED, "rows": 0, "q": None, "out": None, "max_new": 0}
+    assert lib.kivi_paged_attention(*a.values()) == 0
+    assert N.STATUS[lib.kivi_paged_attention(*{**a, "max_new": -1}.values())] == "KIVI_ERR_INVALID_ARG"
