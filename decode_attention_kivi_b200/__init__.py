@@ -418,7 +418,7 @@ class PagedCache:
         self.num_free = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
         self.offsets = torch.zeros(max_requests + 1, dtype=torch.int32, device=dev)
         self.slots = self.positions = torch.zeros(0, dtype=torch.int32, device=dev)
-        self._rows = {}  # slots and positions of each number of rows that a step has had
+        self._rows = {}  # the buffers of slots and positions, by their size
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.workspace = torch.zeros(n, dtype=torch.uint8, device=dev)
         self.max_new = 1
@@ -429,10 +429,13 @@ class PagedCache:
         packed rows in the step's buffers (none where all requests are idle or released), of which no
         request has more than max_new."""
         if rows != self.slots.numel():
-            if rows not in self._rows:  # kept for good: a captured step holds their addresses
-                self._rows[rows] = tuple(_empty((rows,), torch.int32, self.lengths.device, stream)
+            # kept for good, since a captured step holds their addresses: one pair of buffers for each
+            # power of two of rows, less than four times the largest step's in all
+            size = 1 << max(rows - 1, 0).bit_length()
+            if size not in self._rows:
+                self._rows[size] = tuple(_empty((size,), torch.int32, self.lengths.device, stream)
                                          for _ in range(2))
-            self.slots, self.positions = self._rows[rows]
+            self.slots, self.positions = (x[:rows] for x in self._rows[size])
         self.max_new = max(1, rows if max_new is None else max_new)  # a step may have no row
         kivi_paged_assign(self.lengths, new_tokens, self.block_table, self.free_pages,
                           self.num_free, self.page_size, kv_lengths=self.lengths,

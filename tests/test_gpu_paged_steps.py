@@ -46,3 +46,21 @@ def test_steps_without_rows(kivi, largest):
     keys, values = (torch.cat([first[i][40:49], x]) for i, x in ((1, k), (2, v)))
     U.assert_close(out, *U.attend(q, keys, values), "the request that stayed")
     assert cache.check_device_status() == 0
+
+
+def test_steps_of_many_sizes_hold_little_memory(kivi):
+    """Slots and positions of every number of rows up to 200: few buffers, whose addresses stay."""
+    cache, at, seen = small_cache(kivi), {}, set()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for rows in [*range(1, 201), *range(200, 0, -7), 0, 64]:
+        cache.assign(ints([0, 0, 0]), rows)
+        assert cache.slots.shape == cache.positions.shape == (rows,)
+        assert cache.slots.tolist() == [-1] * rows and cache.positions.tolist() == [0] * rows
+        if rows:
+            where = cache.slots.data_ptr(), cache.positions.data_ptr()
+            assert at.setdefault(rows, where) == where
+            seen.add(where)
+    assert len(seen) <= 9
+    # nine sizes of 2 arrays of at most 512 bytes to 1 KB (the allocator's granule is 512 bytes)
+    assert torch.cuda.memory_allocated() - before <= 9 * 2 * 1024
