@@ -7,6 +7,13 @@ streams.  There is no CPU fallback: if the library is missing, calls raise.
 
 ``KiviCache`` is a convenience owner of the device buffers (allocated with
 torch) around one handle.
+
+Calls are asynchronous on ``stream`` (None: torch's current one); a
+``torch.cuda.Stream`` or a raw handle.  What a call reads has to be ready there,
+and its tensors have to live until that stream has run it.  The calls of the
+paged cache and of packed rows see to the second themselves for a
+``torch.cuda.Stream`` (they record their tensors on it); with a raw handle, an
+``ExternalStream``, or the other calls, the caller keeps the tensors.
 """
 from __future__ import annotations
 
@@ -287,9 +294,12 @@ class Bf16Attention:
 
 # ---- the paged 16-bit cache and attention over packed rows ----
 
-def _raw_stream(stream) -> int | None:
-    """None for the current stream, which the binding asks for itself."""
-    return None if stream is None else _stream(stream)
+def _call_stream(stream):
+    """None (the current stream, which the binding asks for itself), a torch stream, on which the
+    binding records the call's tensors, or the handle of a stream that is not torch's own."""
+    if stream is None or type(stream) is torch.cuda.Stream:
+        return stream
+    return _stream(stream)
 
 
 def _on(stream, device):
@@ -336,7 +346,7 @@ def kivi_paged_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_tab
     [rows].  Negative new_tokens release a request.  All int32; `status` [1] collects failures."""
     check(binding().assign(lengths, new_tokens, block_table, free_pages, num_free, page_size,
                            kv_lengths, num_free_out, offsets, slots, positions, status,
-                           _raw_stream(stream)), "kivi_paged_assign")
+                           _call_stream(stream)), "kivi_paged_assign")
 
 
 def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
@@ -344,7 +354,7 @@ def kivi_paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Ten
                       status: torch.Tensor | None = None, stream=None) -> None:
     """Writes k_new, v_new [rows][Hkv][D] into the slots [rows] of one layer's pages
     [num_pages][Hkv][page_size][D] (bf16 or fp16); rows with a negative slot are skipped."""
-    check(binding().append(k_new, v_new, slots, k_pages, v_pages, status, _raw_stream(stream)),
+    check(binding().append(k_new, v_new, slots, k_pages, v_pages, status, _call_stream(stream)),
           "kivi_paged_append")
 
 
@@ -357,7 +367,7 @@ def kivi_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     behind the last request are left as they were."""
     if stream is not None and out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
-    got = binding().packed(q, k, v, offsets, workspace, out, sm_scale, _raw_stream(stream))
+    got = binding().packed(q, k, v, offsets, workspace, out, sm_scale, _call_stream(stream))
     if type(got) is int:
         check(got, "kivi_packed_attention")
     return got
@@ -375,7 +385,7 @@ def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     if stream is not None and out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
     got = binding().paged(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, max_new,
-                          out, sm_scale, _raw_stream(stream))
+                          out, sm_scale, _call_stream(stream))
     if type(got) is int:
         check(got, "kivi_paged_attention")
     return got

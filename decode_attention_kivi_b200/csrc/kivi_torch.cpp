@@ -9,9 +9,11 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -30,6 +32,8 @@ decltype(&kivi_paged_attention) f_paged;
 struct Call {
   bool ok = true;
   int device = -2;
+  int count = 0;
+  const at::Tensor* used[16];  // of a call; some twice
 
   template <typename... A>
   void fail(const char* format, A... args) {
@@ -54,6 +58,7 @@ struct Call {
       fail("%s: tensors must be CUDA tensors", name);
     else if (dev != device)
       fail("tensors on cuda:%d and cuda:%d: one device is needed", device, dev);
+    if (ok) used[count++] = &t;
     return &t;
   }
   // The call runs on the current device, whose stream it takes.
@@ -81,12 +86,30 @@ struct Call {
       fail("%s: heads and channels of a row must be contiguous", name);
     return t->size(0) < 2 ? heads * dim : t->stride(0);
   }
+  // The call's stream, asked for last: the current one, a torch stream, or a handle.  Torch is told
+  // that the tensors are used on a stream of its own other than the current one, so that the caller
+  // may drop them right after the call.  A handle may be gone by the time a tensor is dropped, so the
+  // caller keeps the tensors until that stream has run the call.
   void* stream(PyObject* o) {
     if (!ok) return nullptr;
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-    void* s = PyLong_AsVoidPtr(o);
-    if (PyErr_Occurred()) ok = false;
-    return s;
+    const auto current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device);
+    if (o == Py_None) return current.stream();
+    if (!THPStream_Check(o)) {
+      void* s = PyLong_AsVoidPtr(o);
+      if (PyErr_Occurred()) ok = false;
+      return s;
+    }
+    const auto* t = reinterpret_cast<THPStream*>(o);
+    const auto s = c10::cuda::CUDAStream::unpack3(
+        t->stream_id, (c10::DeviceIndex)t->device_index, (c10::DeviceType)t->device_type);
+    if (s.device_index() != device) {
+      fail("stream on cuda:%d, but the tensors are on cuda:%d", (int)s.device_index(), device);
+      return nullptr;
+    }
+    if (s != current)
+      for (int i = 0; i < count; ++i)
+        c10::cuda::CUDACachingAllocator::recordStream(used[i]->storage().data_ptr(), s);
+    return s.stream();
   }
   int32_t int32(PyObject* o) {
     if (!ok) return 0;

@@ -64,3 +64,65 @@ def test_steps_of_many_sizes_hold_little_memory(kivi):
     assert len(seen) <= 9
     # nine sizes of 2 arrays of at most 512 bytes to 1 KB (the allocator's granule is 512 bytes)
     assert torch.cuda.memory_allocated() - before <= 9 * 2 * 1024
+
+
+@pytest.mark.parametrize("op", ["packed", "paged", "append", "assign"])
+def test_tensors_dropped_right_after_a_call_on_another_stream(kivi, op):
+    """Inputs dropped while the call's stream is still busy: their memory is not handed out before
+    the call has read them."""
+    gen, stream = gen_of(61), torch.cuda.Stream()
+    n, hkv, hq, dim, page = 4096, 2, 4, 64, 16
+    ws = torch.zeros(kivi.kivi_attention_workspace_bytes(hkv, hq, dim), dtype=torch.uint8,
+                     device="cuda")
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None]
+
+    def inputs():
+        g = gen_of(62)
+        q, k, v = (torch.randn(n, h, dim, generator=g, device="cuda").to(BF16)
+                   for h in (hq, hkv, hkv))
+        if op == "packed":
+            return q, k, v, ints([0, n])
+        if op == "append":
+            return k, v, torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+        if op == "assign":
+            return (ints([1] * 3000),)
+        pages = [x.view(n // page, page, hkv, dim).transpose(1, 2).contiguous() for x in (k, v)]
+        return q[-1:].clone(), *pages, table.clone(), ints([n]), ints([0, 1])
+
+    def results():
+        if op == "append":
+            return [torch.zeros(n // page, hkv, page, dim, dtype=BF16, device="cuda")
+                    for _ in range(2)]
+        if op == "assign":
+            z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+            return [z(3000), z(1), z(3001), z(3000), z(3000), z(1), z(3000, 1),
+                    torch.arange(3000, dtype=torch.int32, device="cuda"), ints([3000])]
+        return [torch.zeros(n if op == "packed" else 1, hq, dim, dtype=BF16, device="cuda")]
+
+    def call(x, out, stream=None):
+        if op == "packed":
+            kivi.kivi_packed_attention(*x, ws, out=out[0], stream=stream)
+        elif op == "paged":
+            kivi.kivi_paged_attention(*x, ws, max_new=1, out=out[0], stream=stream)
+        elif op == "append":
+            kivi.kivi_paged_append(*x, *out, stream=stream)
+        else:
+            kv, nf, off, slots, pos, status, t, free, num_free = out
+            kivi.kivi_paged_assign(torch.zeros_like(kv), x[0], t, free, num_free, page,
+                                   kv_lengths=kv, num_free_out=nf, offsets=off, slots=slots,
+                                   positions=pos, status=status, stream=stream)
+
+    want, got = results(), results()
+    call(inputs(), want)
+    x = inputs()
+    shapes = [(t.shape, t.dtype) for t in x]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+    call(x, got, stream)
+    del x
+    junk = [torch.empty(s, dtype=t, device="cuda").fill_(3) for s, t in shapes]
+    torch.cuda.synchronize()
+    assert len(junk) == len(shapes)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
