@@ -117,9 +117,11 @@ _binding = None
 
 def binding():
     """The native binding of the paged-cache and packed-attention calls (csrc/kivi_torch.cpp),
-    calling the library that lib() loaded; raises if it has not been built."""
+    calling the library that lib() loaded; raises if it has not been built for the torch and the
+    Python that run."""
     global _binding
     if _binding is None:
+        from . import build
         path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kivi_torch.so")
         if not os.path.exists(path):
             raise RuntimeError(
@@ -128,6 +130,10 @@ def binding():
         spec = importlib.util.spec_from_loader("_kivi_torch", loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
+        if module.target != build.binding_target():
+            raise RuntimeError(
+                f"{path} is built for {module.target}, not for {build.binding_target()}: build it "
+                "with `python -m decode_attention_kivi_b200.build`")
         L = lib()
         module.library(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "kivi_paged_assign", "kivi_paged_append", "kivi_packed_attention",

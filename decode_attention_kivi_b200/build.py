@@ -2,6 +2,7 @@
 _kivi_torch.so (the tensor checks and calls of the paged-cache binding) with g++."""
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -13,6 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkivi.so")
 BINDING = os.path.join(PKG, "_kivi_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "kivi_torch.cpp")
+BINDING_TARGET = os.path.join(PKG, "_build", "binding_target")  # what the binding was built for
 DEBUG_LIB = os.path.join(PKG, "libkivi_debug.so")
 # debug build: short bounded waits (about 1 ms), copy bounds checks, a test hook
 DEBUG_FLAGS = ["-DKIVI_DEBUG_BUILD", "-DKIVI_DEBUG_BOUNDS", "-DKIVI_DEBUG_WAIT_CYCLES=2000000LL"]
@@ -41,11 +43,24 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def binding_target() -> str:
+    """The torch and the Python that a binding is built for: their interfaces change by release."""
+    return f"torch {importlib.metadata.version('torch')}, Python {sysconfig.get_python_version()}"
+
+
+def binding_stale() -> bool:
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_TARGET):
+        return True
+    with open(BINDING_TARGET) as f:
+        if f.read() != binding_target():
+            return True
+    inputs = [BINDING_SOURCE, os.path.join(ROOT, "include", "kivi.h")]
+    return any(os.path.getmtime(f) > os.path.getmtime(BINDING) for f in inputs)
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Builds _kivi_torch.so against the torch that is installed, when stale."""
-    inputs = [BINDING_SOURCE, os.path.join(ROOT, "include", "kivi.h")]
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+    if not force and not binding_stale():
         return BINDING
     import torch
     from torch.utils.cpp_extension import include_paths
@@ -54,6 +69,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     tmp = BINDING + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DKIVI_BINDING_TARGET="{binding_target()}"',
            *[f"-I{d}" for d in dirs], BINDING_SOURCE, "-o", tmp,
            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -61,6 +77,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_TARGET), exist_ok=True)
+    with open(BINDING_TARGET, "w") as f:
+        f.write(binding_target())
     return BINDING
 
 

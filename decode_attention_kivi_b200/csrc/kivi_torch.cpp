@@ -365,4 +365,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kivi_torch", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kivi_torch() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__kivi_torch() {
+  PyObject* m = PyModule_Create(&module);
+  // what the build compiled this for, for the loader's check
+  if (m != nullptr && PyModule_AddStringConstant(m, "target", KIVI_BINDING_TARGET) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -171,3 +171,28 @@ def test_paged_attention_without_rows_takes_a_max_new_of_zero(lib):
     a = {**PAGED, "rows": 0, "q": None, "out": None, "max_new": 0}
     assert lib.kivi_paged_attention(*a.values()) == 0
     assert N.STATUS[lib.kivi_paged_attention(*{**a, "max_new": -1}.values())] == "KIVI_ERR_INVALID_ARG"
+
+
+# ---- the binding's build ----
+
+def test_a_binding_for_another_torch_is_built_again(lib, monkeypatch, tmp_path):
+    """With nothing newer among the sources: another torch alone makes it stale."""
+    assert not B.binding_stale()
+    ran = []
+    with monkeypatch.context() as m:
+        m.setattr(B, "binding_target", lambda: "torch 0.1, Python 3.0")
+        m.setattr(B, "BINDING_TARGET", str(tmp_path / "_build" / "target"))
+        m.setattr(B.os, "replace", lambda a, b: None)
+        m.setattr(B.subprocess, "run", lambda cmd, check: ran.append(cmd))
+        B.build_binding()
+        assert len(ran) == 1 and any("torch 0.1" in a for a in ran[0])
+        B.build_binding()
+        assert len(ran) == 1
+    assert not B.binding_stale()
+
+
+def test_a_binding_for_another_torch_is_refused(lib, monkeypatch):
+    monkeypatch.setattr(N, "_binding", None)
+    monkeypatch.setattr(B, "binding_target", lambda: "torch 0.1, Python 3.0")
+    with pytest.raises(RuntimeError, match="built for torch"):
+        N.binding()
