@@ -620,7 +620,10 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
       }
       p = nx;
     }
-    if (!ok) fail();
+    if (!ok) {
+      asm volatile("cp.async.wait_all;" ::: "memory");  // Q rows on their way
+      fail();
+    }
     if (!join_here && threadIdx.x == 0) reinterpret_cast<Cut*>(a.partials)[cta] = cut;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
