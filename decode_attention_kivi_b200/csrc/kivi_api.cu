@@ -14,6 +14,7 @@
 #include "kivi_kernels.h"
 #include "kivi_launch.cuh"
 #include "kivi_layout.cuh"
+#include "kivi_paged.h"
 #include "kivi_status.h"
 
 struct kivi_cache {
@@ -718,6 +719,9 @@ extern "C" kivi_status kivi_static_scratch_status(void* stream, uint32_t* code_o
 #include "../../include/kivi_debug.h"
 
 extern "C" kivi_status kivi_debug_overstate_copies(uint32_t bytes) {
-  return from_cuda(kivi::debug_overstate_copies(bytes));
+  cudaError_t e = kivi::debug_overstate_copies(bytes);
+  if (e == cudaSuccess) e = kivi::debug_overstate_varlen(bytes);
+  if (e == cudaSuccess) e = kivi::debug_overstate_paged_decode(bytes);
+  return from_cuda(e);
 }
 #endif

@@ -83,4 +83,10 @@ long varlen_partial_bytes(int D);
 cudaError_t launch_paged_decode(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream);
 long paged_decode_partial_bytes(int D);
 
+#ifdef KIVI_DEBUG_BUILD
+// Bytes added to every copy size that the two attention kernels expect (kivi_debug.h).
+cudaError_t debug_overstate_varlen(unsigned bytes);
+cudaError_t debug_overstate_paged_decode(unsigned bytes);
+#endif
+
 }  // namespace kivi

@@ -244,7 +244,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       }
       const int n = __popc(__ballot_sync(0xffffffffu, mine));
       unsigned char* st = smem + s * C::kStageBytes;
-      if (lane == 0) mbar_expect_tx(&full[s], n * rows * 2 * D);
+      if (lane == 0) mbar_expect_tx(&full[s], n * rows * 2 * D + debug_overstate());
       __syncwarp();
       if (mine)
         tma_load_3d(st + is_v * C::kTileBytes + part * rows * 2 * D, map, 0, y, 0, &full[s]);
@@ -554,6 +554,12 @@ cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t str
 }  // namespace
 
 long paged_decode_partial_bytes(int D) { return (long)kMaxGrid * 2 * kDecodeRows * (D + 2) * 4; }
+
+#ifdef KIVI_DEBUG_BUILD
+cudaError_t debug_overstate_paged_decode(unsigned bytes) {
+  return cudaMemcpyToSymbol(g_debug_overstate, &bytes, sizeof bytes);
+}
+#endif
 
 cudaError_t launch_paged_decode(const VarlenAttnArgs& a, float scale_log2, cudaStream_t stream) {
   if (!is_short(a.max_new, a.Hq / a.Hkv)) return cudaErrorInvalidValue;

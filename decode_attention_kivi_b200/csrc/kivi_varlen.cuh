@@ -63,6 +63,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// Debug build only: bytes added to every copy size that the kernels of the including file expect on
+// their mbarriers (kivi_debug.h).
+#ifdef KIVI_DEBUG_BUILD
+static __device__ unsigned g_debug_overstate = 0u;
+__device__ __forceinline__ uint32_t debug_overstate() { return g_debug_overstate; }
+#else
+__device__ __forceinline__ uint32_t debug_overstate() { return 0u; }
+#endif
+
 // mbar_wait_bounded, given up early once another role of the block set `abort`.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
                                                   const volatile int* abort) {

@@ -768,7 +768,7 @@ varlen_attention_kernel(const __grid_constant__ CUtensorMap tk,
               break;
             }
             unsigned char* dst = smem + C::kOffRing + s * C::kTileBytes;
-            if (lane == 0) mbar_expect_tx(&full[s], n * box * 128);
+            if (lane == 0) mbar_expect_tx(&full[s], n * box * 128 + debug_overstate());
             __syncwarp();
             if (mine) tma_load_2d(dst + slab * kSlabV + part * box * 128, v ? &tv : &tk, x, y, &full[s]);
           }
@@ -936,6 +936,12 @@ long varlen_partial_bytes(int D) {
   const long decode = paged_decode_partial_bytes(D);
   return here > decode ? here : decode;
 }
+
+#ifdef KIVI_DEBUG_BUILD
+cudaError_t debug_overstate_varlen(unsigned bytes) {
+  return cudaMemcpyToSymbol(g_debug_overstate, &bytes, sizeof bytes);
+}
+#endif
 
 cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream) {
   const float scale = (a.sm_scale > 0.f ? a.sm_scale : 1.f / std::sqrt((float)a.D)) * kLog2eV;
