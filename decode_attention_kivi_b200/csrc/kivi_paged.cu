@@ -74,6 +74,14 @@ __device__ __forceinline__ int find_request(const int* prefix, int B, int x) {
   return lo;
 }
 
+// The slot of position pos in page id; -1, reported, where the id is negative or its slot no int.
+__device__ __forceinline__ int slot_of(const PagedAssignArgs& a, int id, int pos) {
+  const long long s = ((long long)id << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+  if (id >= 0 && s <= INT_MAX) return (int)s;
+  atomicOr(a.status, kPagedBadPage);
+  return -1;
+}
+
 __global__ void __launch_bounds__(kAssignThreads)
 paged_assign_kernel(PagedAssignArgs a, bool rows_here) {
   wait_for_predecessor();
@@ -178,8 +186,7 @@ paged_assign_kernel(PagedAssignArgs a, bool rows_here) {
       const int have = (s_len[b] + page - 1) >> a.page_shift, p = pos >> a.page_shift;
       const int id = p < have ? a.table[(long)b * a.width + p]
                               : stack((int)top - 1 - (s_need[b] + p - have));
-      const long long s = ((long long)id << a.page_shift) + (pos & (page - 1));
-      slot = id < 0 || s > INT_MAX ? -1 : (int)s;
+      slot = slot_of(a, id, pos);
     }
     a.slots[i] = slot;
     a.positions[i] = pos;
@@ -196,7 +203,7 @@ paged_rows_kernel(PagedAssignArgs a) {
   __syncthreads();
   const long first = 4 * ((long)blockIdx.x * blockDim.x + threadIdx.x);
   if (first >= a.rows) return;
-  const int i0 = (int)first, n = a.rows - i0 < 4 ? a.rows - i0 : 4, page = 1 << a.page_shift;
+  const int i0 = (int)first, n = a.rows - i0 < 4 ? a.rows - i0 : 4;
   const int total = s_off[a.B];
   // the request of the first row, and from there on the next ones
   int b = i0 < total ? find_request(s_off, a.B, i0) : a.B;
@@ -206,9 +213,7 @@ paged_rows_kernel(PagedAssignArgs a) {
     if (i < total) {
       while (s_off[b + 1] <= i) ++b;
       pos = a.kv_lengths[b] - (s_off[b + 1] - i);
-      const int id = a.table[(long)b * a.width + (pos >> a.page_shift)];
-      const long long s = ((long long)id << a.page_shift) + (pos & (page - 1));
-      slot = id < 0 || s > INT_MAX ? -1 : (int)s;
+      slot = slot_of(a, a.table[(long)b * a.width + (pos >> a.page_shift)], pos);
     }
     a.slots[i] = slot;
     a.positions[i] = pos;

@@ -427,7 +427,8 @@ kivi_status kivi_fake_quant_keys(const void* k, int64_t rows, int32_t head_dim, 
  *   status: a word as above.  If the pages do not suffice (8), or a length, the
  *     new rows (more than `rows`) or the free count do not fit (4), nothing
  *     changes: kv_lengths and num_free_out repeat the old values, offsets are 0
- *     and slots -1, so the step's other calls do nothing.
+ *     and slots -1, so the step's other calls do nothing.  A row whose page id is
+ *     negative, or too large for a slot, has a slot of -1 (2); the step is made.
  * Apart from the two pairs named the arrays must not overlap.
  * Errors: INVALID_ARG (NULL or unaligned pointers, counts, table_width * page_size
  * or num_pages * page_size >= 2^31 - 256), UNSUPPORTED (page_size, batch), CUDA. */

@@ -126,3 +126,22 @@ def test_tensors_dropped_right_after_a_call_on_another_stream(kivi, op):
     assert len(junk) == len(shapes)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [40, 3000])
+def test_assign_reports_bad_page_ids(kivi, rows):
+    """A table entry and a free page that are no page ids: their rows' slots are -1 and bit 2 is set,
+    by the one kernel and by the rows' own; the other rows are as ever."""
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for bad in (-3, 2 ** 31 - 1):
+        table, free = z(3, 4), ints([7, bad, 9])
+        table[0, 0], table[1, 0] = bad, 5
+        lengths, status, slots, positions = ints([5, 15, 0]), z(1), z(rows) - 7, z(rows)
+        kivi.kivi_paged_assign(lengths, ints([2, 3, 4]), table, free, ints([3]), 16,
+                               kv_lengths=lengths, num_free_out=z(1), offsets=z(4), slots=slots,
+                               positions=positions, status=status)
+        # request 0 goes on in its bad page; 1 fills its page and pops 9; 2 pops the bad one
+        assert slots[:9].tolist() == [-1, -1, 95, 144, 145, -1, -1, -1, -1]
+        assert positions[:9].tolist() == [5, 6, 15, 16, 17, 0, 1, 2, 3]
+        assert (slots[9:] == -1).all() and status.item() == 2
+        assert lengths.tolist() == [7, 18, 4] and table[1:, :2].tolist() == [[5, 9], [bad, 0]]
