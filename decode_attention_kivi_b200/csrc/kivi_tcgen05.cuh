@@ -222,7 +222,10 @@ __device__ __forceinline__ void ld_x64(uint32_t taddr, float (&v)[64]) {
 
 // Warp-collective store of 32 consecutive fp32 columns per lane (see ld_x32);
 // complete after wait_st.
-__device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void st_x32(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
       "%1,%2,%3,%4,%5,%6,%7,%8,"
@@ -240,13 +243,7 @@ __device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t (&r)[32]) 
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void st_x32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
-  st_x32(taddr, r);
-}
-// As st_x32 for 16 columns.
+// As st_x32 for 16 columns of 32 bits each.
 __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
