@@ -145,3 +145,20 @@ def test_assign_reports_bad_page_ids(kivi, rows):
         assert positions[:9].tolist() == [5, 6, 15, 16, 17, 0, 1, 2, 3]
         assert (slots[9:] == -1).all() and status.item() == 2
         assert lengths.tolist() == [7, 18, 4] and table[1:, :2].tolist() == [[5, 9], [bad, 0]]
+
+
+def test_the_pages_hold_what_the_steps_appended(kivi):
+    """Each request's tokens, read back by its table, over steps with releases between."""
+    gen, cache = gen_of(71), small_cache(kivi, num_pages=20)
+    keys, values = ([torch.empty(0, 2, 64, dtype=BF16, device="cuda")] * 3 for _ in range(2))
+    for new in ([40, 9, 70], [1, 1, 1], [-1, 30, 1], [17, 1, 0], [1, -1, 60], [3, 100, 1]):
+        k, v = step(cache, gen, new, pad=1)[1:3]
+        off = cache.offsets.tolist()
+        for b, n in enumerate(new):
+            for held, x in ((keys, k), (values, v)):
+                held[b] = torch.cat([held[b], x[off[b]:off[b + 1]]]) if n >= 0 else held[b][:0]
+            length = keys[b].shape[0]
+            assert cache.lengths[b].item() == length
+            assert torch.equal(U.gather(cache.k_pages[0], cache.block_table[b], length), keys[b])
+            assert torch.equal(U.gather(cache.v_pages[0], cache.block_table[b], length), values[b])
+    assert cache.check_device_status() == 0
