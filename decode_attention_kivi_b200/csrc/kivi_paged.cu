@@ -226,7 +226,8 @@ paged_rows_kernel(PagedAssignArgs a) {
 // one wave of blocks that fills the SMs; 24.5 us by two, 25.5 by as many as there are vectors.
 // One 16-byte vector of K and V per thread and step; a token's row of Hkv * D
 // values is contiguous in the input and one run of D values per head in its page.
-__global__ void __launch_bounds__(256)
+constexpr int kAppendThreads = 256, kThreadsPerSm = 2048;
+__global__ void __launch_bounds__(kAppendThreads)
 paged_append_kernel(PagedAppendArgs a) {
   wait_for_predecessor();
   const int vec_head = a.D / 8, vec_row = a.Hkv * vec_head;
@@ -282,10 +283,18 @@ cudaError_t launch_paged_assign(const PagedAssignArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
+  int wave = 0;  // blocks that fill the SMs
+  const cudaError_t e = per_device_setup(a.device, &wave, [&](int* v) {
+    int sms = 0;
+    const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, a.device);
+    *v = sms * (kThreadsPerSm / kAppendThreads);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
   const long total = (long)a.T * a.Hkv * (a.D / 8);
-  const long blocks = (total + 255) / 256;
-  return launch_pdl(paged_append_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)),
-                    dim3(256), 0, stream, a);
+  const long blocks = (total + kAppendThreads - 1) / kAppendThreads;
+  return launch_pdl(paged_append_kernel, dim3((unsigned)(blocks < wave ? blocks : wave)),
+                    dim3(kAppendThreads), 0, stream, a);
 }
 
 }  // namespace kivi

@@ -50,6 +50,7 @@ struct PagedAppendArgs {
   uint32_t* status;   // or null
   long k_stride, v_stride;
   int T, Hkv, D, num_pages, page_shift;
+  int device;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 

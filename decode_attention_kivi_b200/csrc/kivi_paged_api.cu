@@ -156,6 +156,7 @@ kivi_status kivi_paged_append(const void* k_new, int64_t k_stride, const void* v
   a.Hkv = num_kv_heads;
   a.D = head_dim;
   a.num_pages = num_pages;
+  if (cudaGetDevice(&a.device) != cudaSuccess) return KIVI_ERR_CUDA;
   return from_cuda(kivi::launch_paged_append(a, static_cast<cudaStream_t>(stream)));
 }
 
