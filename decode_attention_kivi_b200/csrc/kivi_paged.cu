@@ -13,10 +13,11 @@
 // read of F and of the table that another CTA would have written is resolved
 // from the prefix sums instead, so one cluster barrier is enough: the one
 // between the reads of the lengths and the writes of the new lengths, which may
-// be the same array.  A cluster is too few threads for the rows of a large step:
-// above kRowsHere rows a second kernel fills slots and positions from the new
-// tables, four rows per thread (65,000 rows of 500 requests: 9.5 us, 24.5 by the
-// cluster alone).
+// be the same array.  A cluster of eight is never slower than one CTA (16
+// requests, 16 rows: 4.0 for 4.1 us; 1,000 rows: 4.2 for 4.7; 2,000 requests: 8.8
+// for 12.2), but too few threads for the rows of a large step: above kRowsHere
+// rows a second kernel fills slots and positions from the new tables, four rows
+// per thread (measured at the constant).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -32,7 +33,11 @@ namespace cg = cooperative_groups;
 
 constexpr int kAssignThreads = 512;
 constexpr int kAssignCluster = 8;
-constexpr int kRowsHere = 2048;
+// Rows that the cluster fills itself, for those of the second kernel: 16 requests, 16,000 rows 5.2
+// for 6.6 us, 24,000 rows 6.2 for 6.4, 65,000 rows 11.8 for 6.5; 500 requests, 8,000 rows 5.7 for 7.9,
+// 16,000 rows 7.4 for 7.7, 24,000 rows 8.4 for 7.8, 65,000 rows 15.7 for 7.8; 4,096 requests, 8,000 rows
+// 15.5 for 21.9, 32,000 rows 21.5 for 21.5 (in a graph, back to back).
+constexpr int kRowsHere = 16384;
 
 // Exclusive prefix sums of three counts over the block's threads, and the totals.
 struct Counts {
@@ -262,15 +267,14 @@ cudaError_t launch_paged_assign(const PagedAssignArgs& a, cudaStream_t stream) {
                                 (int)(sizeof(int) * (4 * (size_t)kMaxRequests + 3)));
   });
   if (e != cudaSuccess) return e;
-  const int cluster = a.rows > 2 * kAssignThreads || a.B > kAssignThreads ? kAssignCluster : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster);
+  cfg.gridDim = dim3(kAssignCluster);
   cfg.blockDim = dim3(kAssignThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  attr[0].val.clusterDim = {kAssignCluster, 1, 1};
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;

@@ -5,6 +5,7 @@ import torch
 
 import paged_util as U
 from gpu_util import load_kivi
+import test_gpu_paged
 from test_gpu_paged import BF16, gen_of, ints, randn
 
 pytestmark = pytest.mark.gpu
@@ -128,7 +129,14 @@ def test_tensors_dropped_right_after_a_call_on_another_stream(kivi, op):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("rows", [40, 3000])
+@pytest.mark.parametrize("B,page,width,rows", [(40, 64, 60, 16384), (40, 64, 60, 20000),
+                                               (1, 16, 3000, 17001), (4096, 16, 8, 30000)])
+def test_assign_of_many_rows(kivi, B, page, width, rows):
+    """Around the number of rows from which a second kernel fills slots and positions."""
+    test_gpu_paged.test_assign_over_steps(kivi, B, page, width, rows, 3)
+
+
+@pytest.mark.parametrize("rows", [40, 3000, 20000])
 def test_assign_reports_bad_page_ids(kivi, rows):
     """A table entry and a free page that are no page ids: their rows' slots are -1 and bit 2 is set,
     by the one kernel and by the rows' own; the other rows are as ever."""
