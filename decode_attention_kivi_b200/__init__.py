@@ -381,7 +381,8 @@ def kivi_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     """Attention of each request's new rows (q [rows][Hq][D], request b in rows offsets[b] ..
     offsets[b+1]-1) over its kv_lengths[b] keys in the pages of block_table[b], causal, the new
     tokens being the last keys -> out like q.  max_new: no request has more new rows (1 in a
-    decode step; by default the number of rows)."""
+    decode step; by default the number of rows, and then a decode step takes the kernel for chunks,
+    which is slower for single tokens)."""
     if stream is not None and out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
     got = binding().paged(q, k_pages, v_pages, block_table, kv_lengths, offsets, workspace, max_new,
@@ -437,7 +438,7 @@ class PagedCache:
                stream=None) -> None:
         """Starts a step: new_tokens [max_requests] (int32, device; negative releases), `rows`
         packed rows in the step's buffers (none where all requests are idle or released), of which no
-        request has more than max_new."""
+        request has more than max_new (by default `rows`; a decode step is faster with 1)."""
         if rows != self.slots.numel():
             # kept for good, since a captured step holds their addresses: one pair of buffers for each
             # power of two of rows, less than four times the largest step's in all

@@ -227,8 +227,8 @@ paged_rows_kernel(PagedAssignArgs a) {
 
 // ---- append ----
 
-// Bound by HBM: 16,000 rows of 8 heads of 128, 131 MB read and written, in 23.2 us (5.7 TB/s) by
-// one wave of blocks that fills the SMs; 24.5 us by two, 25.5 by as many as there are vectors.
+// Bound by HBM: 16,000 rows of 8 heads of 128, 131 MB read and written, in 23.7 us (5.5 TB/s) by
+// one wave of blocks that fills the SMs; 5% more by two, 10% by as many as there are vectors.
 // One 16-byte vector of K and V per thread and step; a token's row of Hkv * D
 // values is contiguous in the input and one run of D values per head in its page.
 constexpr int kAppendThreads = 256, kThreadsPerSm = 2048;

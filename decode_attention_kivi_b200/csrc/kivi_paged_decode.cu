@@ -23,7 +23,7 @@
 // do not depend on the order of arrival.
 // Every wait is bounded; a wait that runs out sets the status word.
 //
-// 16 requests of up to 8K keys, 32 / 8 heads of 128, pages of 64: 67 to 69 us, 5.4 TB/s
+// 16 requests of up to 8K keys, 32 / 8 heads of 128, pages of 64: 68.6 us, 5.4 TB/s
 // (82% of the measured copy rate); 8 requests to 4K, 32 heads, pages of 16: 59.5 us,
 // 4.9 TB/s.  Of some 130,000 cycles 1,800 are the prologue, 6,000 the way to the
 // first tile (lengths, table, copy, each from DRAM), 6,000 the last item's join.
@@ -42,7 +42,8 @@ constexpr int kBoxD = kTileD * 128; // 64 rows of 64 channels, the swizzle span
 // some 900 cycles, and the last reads p states, for each of its threads' 4-channel groups some 175
 // cycles each, so p = sqrt(5 t / groups) is best (16,000 keys of 16 heads: 66 us at two tiles, 26 at
 // eight, 25 by this rule); then as many tiles as cut the longest item evenly, since a CTA that ends
-// one item and begins the next has two ends to its work (513 keys: 8.4 us at two tiles, 6.8 at three).
+// one item and begins the next has two ends to its work (513 keys: 7.4 us at three tiles, some
+// 15% more at two).
 constexpr int kMinTilesD = 2;
 // log2 of a row's largest weight.  A bf16 weight is rounded relative to itself; a fp16 one has steps
 // of 2^-24 below 2^-14, so that without the factor (which O / l does not see) a long tail of keys near

@@ -49,17 +49,22 @@
 // Every wait is bounded; a wait that runs out sets the status word, and what was
 // issued is drained before TMEM is released.
 //
-// What bounds it (16,384 rows, 32 / 8 heads of 128, bf16): 1.82 ms, 1.21 PFLOP/s,
-// in single passes at 1.75 GHz; 2.09 ms back to back, where the card lowers the
-// clock to hold its power.  A unit of both halves takes 1,780 cycles: its products
+// The weights go into the second product in the element type: the operand in TMEM
+// is 16 bits wide, and two of them to a weight would double that product.  In bf16
+// the outputs are 0.0023 of their size off the 64-bit values where weights of 32
+// bits leave 0.0017, most of it the rounding of the result; fp16 0.00025, 0.00021.
+//
+// What bounds it (16,384 rows, 32 / 8 heads of 128, bf16): 2.13 ms back to back,
+// 1.03 PFLOP/s, where the card lowers the clock to hold its power; single passes
+// after a pause take 1.8 to 1.9 ms (1.75 GHz).  A unit of both halves takes 1,780 cycles: its products
 // 1,280 (a step of the scores is 48 cycles at N = 64, 6 KB of operands at 128
 // bytes a cycle, where its arithmetic takes 32), its exponentials 1,024.  Whole
 // tiles of scores (N = 128, 64 cycles a step, no room for a second buffer) take
-// 1.76 ms here, but 154 us where units take 131 on 8111 rows of 13 prompts, and
-// 140 us for 121 on a step of 32 requests.  Taking a quarter of the exponentials
+// 3% less here, but 18% more on 8111 rows of 13 prompts, and 16% more on a step
+// of 32 requests.  Taking a quarter of the exponentials
 // to the fp32 pipe, fetching the next unit's scores early, warps of their own for
 // the items' ends, and one MMA warp for both halves changed nothing or cost time;
-// so did a lone half's tiles taken in turn by both (the step: 165 us), whose ring
+// so did a lone half's tiles taken in turn by both (the step: 36% more), whose ring
 // then holds too few tiles ahead.
 #include <cmath>
 
@@ -87,8 +92,10 @@ constexpr int kSlabV = 128 * 128;      // 128 rows of 64 channels
 constexpr int kSlots = 4;              // K and V tiles in flight
 constexpr uint32_t kTmemColsV = 512;
 // Half-units per CTA at least (one tile of one item; 4 and 16 took 20% longer on 700 rows of 8
-// prompts), and those that an item's start and end take as long as: 5.7 by a fit over the CTAs of
-// 8111 packed rows of 13 prompts, 32 heads, which take 131 us at 6, 154 at 4, 133 at 8.
+// prompts), and those that an item's start and end take as long as: 5.7 by a fit over the CTAs of 8111
+// packed rows of 13 prompts, 32 heads of 128.  Other costs, against 6, over those rows with 32 x 1, 8 x 4,
+// 2 x 16 and 1 x 64 kv heads by group: at D = 128 4 takes 17, 8, 8 and 10% longer, 8 within 2% of 6, 11
+// up to 4% longer; at D = 64 4 takes 10, 0 and 0% longer, 8 up to 4%, 11 up to 7%.
 constexpr int kMinWorkV = 8;
 constexpr int kItemCost = 6;
 constexpr int kChunk = 32;             // scores turned into weights at a time
@@ -155,9 +162,10 @@ __device__ __forceinline__ int item_tiles(const Request& r, int rows, int tt, co
 }
 
 // Work of a tile of the item, and of an item.  Both halves' units, or the one half's; over pages a
-// lone half's tile counts as three: it waits for its copies as long as both would (the step of the
-// launcher's comment takes 135 us at two, 118 at three, 131 at four; prompts of their own keys, which
-// few of the halves are alone in, take 125 us at two and 131 at three).
+// lone half's tile counts as three: it waits for its copies as long as both would.  Steps of two chunks of
+// 509 rows beside 30 single tokens, 32 x 1, 8 x 4, 2 x 16 and 1 x 64 kv heads by group of 128: at two 7, 13,
+// 19 and 24% longer, at four 20, 11, 5 and 1% (D = 64: 5 to 19% and 6 to 22%).  Prompts of their own keys,
+// which few of the halves are alone in, take 1% longer at three than at two.
 template <bool PAGED>
 __device__ __forceinline__ int tile_work(int rows, int row0) {
   return rows - row0 > kHalf ? 2 * kUnits : kUnits + (PAGED ? 1 : 0);
@@ -910,6 +918,10 @@ cudaError_t launch_t(const VarlenAttnArgs& a, float scale_log2, cudaStream_t str
     return cudaErrorInvalidValue;
   }
   const int grid = a.num_sms < kMaxGrid ? a.num_sms : kMaxGrid;
+  // Cut items joined by their last CTA, from four items per CTA on, or by a second kernel over all SMs:
+  // 64 rows over 16,000 keys (0.1 items per CTA) take 63 us by the first and 36 by the second, 700 rows
+  // of one prompt (0.6) 30 and 23, 1,200 (1) 34 and 33, 2,400 (2) 66.5 and 68, 4,800 (4) 183 and 189,
+  // 7,200 (6) and more the same within their spread; 32 / 8 heads of 128.
   const bool join_here = (long)a.T * a.Hq >= 4L * 2 * kHalf * grid;
   e = launch_pdl(varlen_attention_kernel<T, D, PAGED>, dim3(grid), dim3(kThreadsV), C::bytes(a.B),
                  stream, tk, tv, a, scale_log2, join_here);
@@ -947,7 +959,7 @@ cudaError_t launch_varlen_attention(const VarlenAttnArgs& a, cudaStream_t stream
   const float scale = (a.sm_scale > 0.f ? a.sm_scale : 1.f / std::sqrt((float)a.D)) * kLog2eV;
   // Single tokens go to the decode kernel.  Where some request may have more rows than its tile,
   // all of them come here: 30 decoding requests beside two chunks of 509 rows, contexts of 4K, take
-  // 118 us in one launch and 137 us as the decode kernel and this one in turn.
+  // 127 us in one launch, 16% more as the decode kernel and this one in turn.
   if (a.table != nullptr && is_short(a.max_new, a.Hq / a.Hkv))
     return launch_paged_decode(a, scale, stream);
   return a.dtype == 0 ? launch_form<__nv_bfloat16>(a, scale, stream)
