@@ -468,7 +468,8 @@ kivi_status kivi_attention_workspace_bytes(int32_t num_kv_heads, int32_t num_q_h
  * of the row's largest to 2^-31 of that), the result once.
  *   q, out: [rows][num_q_heads][head_dim]; k, v: [rows][num_kv_heads][head_dim].
  *   sm_scale <= 0 means 1/sqrt(head_dim).
- * Inputs of a request must be finite; rows of no request may hold anything.
+ * Inputs of a request must be finite, and so must sm_scale * log2(e) * <q, k> in 32
+ * bits; rows of no request may hold anything.
  * `out` must not overlap the inputs.  rows * num_q_heads < 2^31 - 512.
  * Errors: INVALID_ARG, UNSUPPORTED, BUFFER_TOO_SMALL (workspace), CUDA. */
 kivi_status kivi_packed_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
