@@ -33,7 +33,6 @@
 namespace kivi {
 namespace {
 
-constexpr float kLog2eD = 1.4426950408889634f;
 constexpr int kTileD = 64;          // keys per tile
 constexpr int kWarpsD = 4;          // consumer warps, 16 keys of each tile
 constexpr int kThreadsD = (kWarpsD + 1) * 32;
