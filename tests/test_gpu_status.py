@@ -82,6 +82,8 @@ def test_older_queries_clear_on_their_stream(kivi, which):
     """The word and a ticket set as a failed call leaves them, the query, and a read at once."""
     query, words = query_of(kivi, which)
     stream = torch.cuda.Stream()
+    if words is not None:
+        words[:64].fill_(0)  # loads the fill's kernel: loading one waits for what runs
     assert query(stream) == 0
     end = busy_default_stream()
     with torch.cuda.stream(stream):
@@ -99,7 +101,9 @@ def test_older_queries_clear_on_their_stream(kivi, which):
 
 def test_a_new_handle_is_clear_on_return(kivi):
     """No clear of a new handle's workspace is pending behind the default stream's work."""
-    small_cache(kivi).close()
+    cache = small_cache(kivi)
+    cache.workspace[:4].fill_(1)
+    cache.close()
     stream = torch.cuda.Stream()
     end = busy_default_stream()
     with torch.cuda.stream(stream):
